@@ -328,7 +328,7 @@ def _handles(s):
             cfg = pm.KV4Config.make(case["hq"], case["hk"], case["d"], page_tokens=case["page"])
             s["cache"] = pm.KV4Cache(cfg, s["n_pages"], buffer=s["buffer"])
             s["batch"] = pm.KV4Batch(s["kv_len"], s["page_table"], s["q_start"], n_tokens=s["tokens"],
-                                     max_q=s["max_q"], max_kv=s["max_kv"])
+                                     max_q=s["max_q"])
     return s["pm"], s["rope"], s.get("cache"), s.get("batch")
 
 
