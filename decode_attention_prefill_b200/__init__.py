@@ -13,6 +13,10 @@ Entry points keep the C names:
     pnmix_decode_attention(cfg, q, cache, out, ws)      decode: attention, fp32 out
 
 ``PNMixCache`` owns the device buffers (cache + decode workspace) of one layer.
+
+Beside it ``KV4Cache`` (kv4.py): a paged cache with every key and value at 4 bits, for
+batches of sequences with any number of new tokens, and ``norm_rope``, the per-head norm and
+rotation that makes the queries and keys of either cache.
 """
 from __future__ import annotations
 
@@ -34,6 +38,9 @@ _lib = ctypes.CDLL(LIB_PATH)
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CAPACITY, ERR_CUDA, ERR_ALIGNMENT, ERR_DEVICE = range(7)
 DEVERR_APPEND_FULL = 0x1
 DEVERR_TIMEOUT = 0x2
+DEVERR_BATCH = 0x4       # pnmix_kv4_*: a row range, length or position out of its bounds
+DEVERR_PAGE = 0x8        # pnmix_kv4_*: a page table entry outside the cache
+DEVERR_NONFINITE = 0x10  # pnmix_kv4_append*: a NaN or a magnitude above 61440 was written
 # decode kernels (Config.decode_kernel)
 DECODE_AUTO, DECODE_SIMT, DECODE_MMA, DECODE_PAIRS, DECODE_TC = range(5)
 DECODE_KERNELS = {"auto": DECODE_AUTO, "simt": DECODE_SIMT, "mma": DECODE_MMA, "ws": DECODE_PAIRS, "tc": DECODE_TC}
@@ -46,6 +53,9 @@ EXPORTED = [
     "pnmix_workspace_bytes_multi", "pnmix_decode_attention_multi", "pnmix_shrink_keys",
     "pnmix_split_groups", "pnmix_debug_decode_stall", "pnmix_workspace_bytes_two",
     "pnmix_decode_attention_two", "pnmix_append_decode",
+    "pnmix_norm_rope", "pnmix_kv4_cache_bytes", "pnmix_kv4_cache_init", "pnmix_kv4_cache_reset",
+    "pnmix_kv4_append", "pnmix_kv4_append_qkv", "pnmix_kv4_read", "pnmix_kv4_workspace_bytes",
+    "pnmix_kv4_attention", "pnmix_kv4_read_error",
 ]
 
 
@@ -415,3 +425,6 @@ def decode_step_host(cache: PNMixCache, q_host: torch.Tensor, k_host: torch.Tens
         pnmix_append(cache.cfg, staging["k"], staging["v"], cache, s)
         pnmix_decode_attention(cache.cfg, staging["q"], cache, out, stream=s)
         out_host.copy_(out, non_blocking=True)
+
+
+from .kv4 import KV4Batch, KV4Cache, KV4Config, Rope, kv4_cache_bytes, kv4_workspace_bytes, norm_rope  # noqa: E402,F401

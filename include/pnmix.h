@@ -150,6 +150,11 @@ typedef enum {
 #define PNMIX_DEVERR_TIMEOUT 0x2u      /* a bounded wait for staged cache data ran out in a
                                           decode call (its output is then invalid); see
                                           pnmix_debug_decode_stall */
+#define PNMIX_DEVERR_BATCH 0x4u        /* pnmix_kv4_*: a row range or a length out of its bounds, or a
+                                          token without a place in the cache */
+#define PNMIX_DEVERR_PAGE 0x8u         /* pnmix_kv4_*: a page table entry outside [0, n_pages) */
+#define PNMIX_DEVERR_NONFINITE 0x10u   /* pnmix_kv4_append*: a NaN or a magnitude above 61440 was
+                                          written (and stored as 0 or +-61440) */
 
 /*
  * Method parameters.  Supported set:
@@ -522,6 +527,192 @@ PNMIX_API pnmix_status pnmix_debug_decode_stall(const pnmix_config* cfg, const u
 
 /* Synchronously read (and, if clear != 0, zero) the device error word.  Host pointer out. */
 PNMIX_API pnmix_status pnmix_read_error(const pnmix_cache* cache, int clear, uint32_t* host_error);
+
+/* ================================================================================
+ * The 4-bit paged cache, and the norm and rotation of queries and keys
+ * ================================================================================
+ *
+ * A second cache form beside the mixed-precision one: every key and value at 4 bits, one
+ * token at a time (no residual window), in pages that a page table hands out, for batches
+ * of sequences with any number of new tokens each.  It has no counterpart in the pages; it
+ * is the uniform 4-bit neighbour of the per-token value scheme above.  The conventions of
+ * every entry point hold.
+ *
+ * Quantizer.  Per token, KV head and run of 32 channels (keys and values alike), in fp32
+ * with one rounding per operation:
+ *     x is taken into [-61440, 61440], a NaN as 0 (both raise PNMIX_DEVERR_NONFINITE);
+ *     s16 = fp16(fl(max - min) / 15), z16 = fp16(min),
+ *     code = clamp(rint((x - z) / s), 0, 15), 0 when s16 == 0;  it stands for code * s + z.
+ * So pages hold finite numbers only, and 15 * s + z is a finite fp16 (61440 = 15 * 2^12:
+ * the largest range, 122880, gives s = 8192 exactly).
+ *
+ * Page layout.  Page p of head h is page_tokens / 16 BLOCKS of 16 tokens each, at
+ *     pages + ((p * n_kv_heads + h) * (page_tokens / 16) + block) * (20 * head_dim).
+ * With n = head_dim / 32 channel groups, a block holds, in this order:
+ *  1. key codes, 8 * head_dim bytes: token t's row at t * head_dim / 2; the row has 4 pieces
+ *     of 4n bytes, piece w one 32-bit word per group g, whose bits [4i, 4i + 4) are the code
+ *     of channel 32g + 8w + i  (i in 0..7);
+ *  2. key scales, 2 * head_dim bytes: per token and group the fp16 pair (scale, zero);
+ *  3. value codes, 8 * head_dim bytes: token t's row at t * head_dim / 2; the row has 8
+ *     pieces of 2n bytes, piece w one 16-bit word per group g, whose bits [4i, 4i + 4) are
+ *     the code of channel 32g + 4w + i  (i in 0..3).  With head_dim 128 piece w of token t
+ *     is stored at place w ^ (4 * (t / 2 % 2));
+ *  4. value scales, as 2.
+ * That is 160 bytes per token and KV head at head_dim 128 (bf16: 512).
+ */
+
+/*
+ * Supported: head_dim 64 or 128; n_q_heads up to 4096, G = n_q_heads / n_kv_heads a whole
+ * number in [1, 128];
+ * page_tokens 16, 32, 64 or 128.  softmax_scale <= 0 selects 1/sqrt(head_dim).
+ */
+typedef struct {
+  int32_t head_dim;
+  int32_t n_q_heads;
+  int32_t n_kv_heads;
+  int32_t page_tokens;
+  float softmax_scale;
+} pnmix_kv4_config;
+
+/* Device pointers into one caller-owned buffer; filled by pnmix_kv4_cache_init. */
+typedef struct {
+  int32_t n_pages;
+  int32_t page_tokens;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  uint8_t* pages;       /* [n_pages][Hkv][page_tokens / 16][20 * head_dim] */
+  uint32_t* error;      /* device error word, behind the pages */
+  void* base;
+  size_t total_bytes;
+} pnmix_kv4_cache;
+
+/*
+ * The sequences of one call.  Token tensors are packed: sequence b owns the rows
+ * [q_start[b], q_start[b+1]) of every one, in order of position; rows from q_start[batch]
+ * on (padding) are neither read nor written.  Its newest row is position kv_len[b] - 1, so
+ * with T rows row j is position kv_len[b] - T + j.  Position x of sequence b is token
+ * x % page_tokens of page page_table[b][x / page_tokens].
+ * The arrays are device memory, read when the call runs.  What they hold cannot be checked
+ * on the host.  The error word says what was wrong (see the bits above), and memory outside
+ * the tensors and the pages is never touched: lengths are clamped to [0, max_pages *
+ * page_tokens]; with a q_start that is not ascending within [0, n_tokens], or a sequence of
+ * more than max_q rows, pnmix_kv4_attention does nothing, and the other calls take rows for
+ * padding or find them another place.
+ */
+typedef struct {
+  int32_t batch;              /* 1 .. 4096 */
+  int32_t n_tokens;           /* rows of the token tensors, >= q_start[batch] */
+  int32_t max_pages;          /* entries of a row of page_table */
+  int32_t max_q;              /* no sequence has more rows than this (1 .. n_tokens) */
+  const int32_t* q_start;     /* [batch + 1], ascending; NULL: n_tokens / batch rows each */
+  const int32_t* kv_len;      /* [batch] tokens in the cache, this call's rows included */
+  const int32_t* page_table;  /* [batch][max_pages]; entries of positions in use are read */
+} pnmix_kv4_batch;
+
+/* A bf16 tensor [tokens][heads][head_dim]: strides in elements, channels contiguous. */
+typedef struct {
+  uint16_t* data;             /* 16-byte aligned */
+  int64_t token_stride;       /* multiples of 8 */
+  int64_t head_stride;
+} pnmix_rows;
+
+/*
+ * Rotation of queries and keys.  Pair i < rot_dim / 2 of a head is the channels
+ * (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved; it turns by the angle
+ * positions[axis[i]][token] * inv_freq[i]; channels from rot_dim on stay.
+ * head_dim 64, 128 or 256; rot_dim a multiple of 16 in [0, head_dim]; n_axes 1 .. 4.
+ */
+typedef struct {
+  int32_t head_dim;
+  int32_t rot_dim;
+  int32_t interleaved;
+  int32_t n_axes;
+  float eps;                  /* of the norm, >= 0 */
+  float inv_freq[128];
+  uint8_t axis[128];          /* < n_axes */
+} pnmix_rope;
+
+/*
+ * Norm of every query and key head and rotation by position, in one pass:
+ *     y = x / sqrt(mean(x^2) + eps) * weight   (weight bf16 [head_dim]; NULL: y = x),
+ *     then every pair (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin),
+ * in fp32 (angles in fp64, reduced to a turn before they are rounded, so far positions keep
+ * their angle), rounded to bf16 once.  n_tokens rows (0 allowed: nothing is done); q and
+ * q_out have n_q_heads heads, k and k_out n_k_heads; either head count may be 0, and its
+ * pointers are then not looked at.  positions: int32 [n_axes][n_tokens], any values.
+ * An output may be its own input (same pointer and strides), otherwise it overlaps none.
+ * Errors: INVALID_ARG (null pointers, negative sizes, an axis >= n_axes, output strides
+ * that let rows overlap), UNSUPPORTED (head_dim, rot_dim or n_axes outside the above),
+ * ALIGNMENT (pointers not 16-byte aligned or strides not multiples of 8).
+ */
+PNMIX_API pnmix_status pnmix_norm_rope(const pnmix_rope* rope, int n_tokens, int n_q_heads, int n_k_heads,
+                                       const pnmix_rows* q, const pnmix_rows* k, const uint16_t* q_weight,
+                                       const uint16_t* k_weight, const int32_t* positions,
+                                       const pnmix_rows* q_out, const pnmix_rows* k_out, void* stream);
+
+/* Bytes of a cache of n_pages pages (the error word included).  Host-only. */
+PNMIX_API pnmix_status pnmix_kv4_cache_bytes(const pnmix_kv4_config* cfg, int n_pages, size_t* total_bytes);
+
+/*
+ * Carve a cache out of `device_base` (>= pnmix_kv4_cache_bytes bytes, 256-byte aligned).
+ * Host-only.  The pages may hold anything (a position is read only after it was written,
+ * unless kv_len says otherwise); pnmix_kv4_cache_reset zeroes them and the error word.
+ */
+PNMIX_API pnmix_status pnmix_kv4_cache_init(const pnmix_kv4_config* cfg, int n_pages, void* device_base,
+                                            size_t bytes, pnmix_kv4_cache* out);
+PNMIX_API pnmix_status pnmix_kv4_cache_reset(const pnmix_kv4_cache* cache, void* stream);
+
+/*
+ * Quantize the batch's rows of k and v ([n_tokens][Hkv][head_dim], after RoPE) into their
+ * places.  A row without a place (a negative position, or one from max_pages * page_tokens
+ * on: PNMIX_DEVERR_BATCH; a page outside the cache: PNMIX_DEVERR_PAGE) is skipped.  A page
+ * that rows of two sequences are written to at the same token is the caller's mistake:
+ * either's codes and scales may stay there.
+ */
+PNMIX_API pnmix_status pnmix_kv4_append(const pnmix_kv4_config* cfg, const pnmix_kv4_batch* batch,
+                                        const pnmix_rows* k, const pnmix_rows* v, pnmix_kv4_cache* cache,
+                                        void* stream);
+
+/*
+ * pnmix_norm_rope of q and k and pnmix_kv4_append of the rotated keys and v in one pass: the
+ * cache and q_out get the same bits as from the two calls (the keys are rounded to bf16
+ * between them).  q, k, v: usually three views of one projection.  positions: int32
+ * [n_axes][n_tokens], apart from the places in the cache.  rope->head_dim is the cache's.
+ */
+PNMIX_API pnmix_status pnmix_kv4_append_qkv(const pnmix_kv4_config* cfg, const pnmix_rope* rope,
+                                            const pnmix_kv4_batch* batch, const pnmix_rows* q,
+                                            const pnmix_rows* k, const pnmix_rows* v,
+                                            const uint16_t* q_weight, const uint16_t* k_weight,
+                                            const int32_t* positions, const pnmix_rows* q_out,
+                                            pnmix_kv4_cache* cache, void* stream);
+
+/*
+ * Read the batch's rows back: bf16(code * s + z) into k_out and v_out.  A row without a
+ * place gets zeros (and raises the bits of pnmix_kv4_append).
+ */
+PNMIX_API pnmix_status pnmix_kv4_read(const pnmix_kv4_config* cfg, const pnmix_kv4_batch* batch,
+                                      const pnmix_kv4_cache* cache, const pnmix_rows* k_out,
+                                      const pnmix_rows* v_out, void* stream);
+
+/*
+ * Causal attention of the batch's query rows over the cached tokens:
+ *     out_r = sum_x softmax_x(q_r . k^_x * scale) v^_x  over x in [0, kv_len[b] - T + j]
+ * for row j of the T rows of sequence b (so a row sees its own token, which was appended
+ * before).  A row that sees no token (kv_len[b] < T - j) gets zeros.  q, out:
+ * [n_tokens][Hq][head_dim].  Sums and softmax in fp32, rounded to bf16 once; see kv4_decode.cu
+ * and kv4_chunk.cu for the fp16 operands inside.  A page outside the cache raises
+ * PNMIX_DEVERR_PAGE and the rows of its sequence are then invalid.
+ * The workspace (pnmix_kv4_workspace_bytes of the same cfg and batch, 256-byte aligned) needs
+ * no initial content and keeps none; calls that may run at the same time need one each.
+ */
+PNMIX_API size_t pnmix_kv4_workspace_bytes(const pnmix_kv4_config* cfg, const pnmix_kv4_batch* batch);
+PNMIX_API pnmix_status pnmix_kv4_attention(const pnmix_kv4_config* cfg, const pnmix_kv4_batch* batch,
+                                           const pnmix_rows* q, const pnmix_kv4_cache* cache,
+                                           const pnmix_rows* out, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+
+/* pnmix_read_error for this cache. */
+PNMIX_API pnmix_status pnmix_kv4_read_error(const pnmix_kv4_cache* cache, int clear, uint32_t* host_error);
 
 /* Static string for a status code. */
 PNMIX_API const char* pnmix_status_string(pnmix_status status);

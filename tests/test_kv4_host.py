@@ -1,0 +1,221 @@
+"""The 4-bit paged cache on the host: refusals before any launch, and the restatement's own
+consistency."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import decode_attention_prefill_b200 as pm
+import kv4_ref as ref
+from decode_attention_prefill_b200 import kv4
+
+B = ctypes.byref
+P = 1 << 41            # a device address that nothing looks at: every call here is refused
+
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="uses fake device pointers; runs only where no kernel "
+                                                              "can launch")
+
+
+def cache(cfg, n_pages=4):
+    c = kv4._Cache()
+    need = pm.kv4_cache_bytes(cfg, n_pages)
+    assert pm._lib.pnmix_kv4_cache_init(B(cfg), n_pages, ctypes.c_void_p(1 << 40), need, B(c)) == pm.OK
+    return c
+
+
+def batch(**kw):
+    d = dict(batch=2, n_tokens=6, max_pages=3, max_q=4, q_start=P, kv_len=P, page_table=P)
+    d.update(kw)
+    return kv4._Batch(*[d[k] for k, _ in kv4._Batch._fields_])
+
+
+def rows(heads=8, D=128, data=P, ts=None, hs=None):
+    return kv4._Rows(data, heads * D if ts is None else ts, D if hs is None else hs)
+
+
+def test_cache_bytes_and_regions():
+    for D in (64, 128):
+        for page in (16, 32, 64, 128):
+            cfg = pm.KV4Config.make(8, 2, D, page)
+            assert pm.kv4_cache_bytes(cfg, 5) == 5 * 2 * page * 20 * D // 16 + 256
+            c = cache(cfg, 5)
+            assert c.error - c.pages == 5 * 2 * page * 20 * D // 16
+    cfg = pm.KV4Config.make(8, 2)
+    c, out = kv4._Cache(), ctypes.c_size_t(0)
+    need = pm.kv4_cache_bytes(cfg, 4)
+    init = pm._lib.pnmix_kv4_cache_init
+    assert init(B(cfg), 4, ctypes.c_void_p((1 << 40) + 16), need, B(c)) == pm.ERR_ALIGNMENT
+    assert init(B(cfg), 4, ctypes.c_void_p(1 << 40), need - 1, B(c)) == pm.ERR_CAPACITY
+    assert init(B(cfg), 0, ctypes.c_void_p(1 << 40), need, B(c)) == pm.ERR_INVALID_ARG
+    assert init(B(cfg), 4, None, need, B(c)) == pm.ERR_INVALID_ARG
+    assert pm._lib.pnmix_kv4_cache_bytes(B(cfg), -1, B(out)) == pm.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("args,status", [
+    (dict(n_q_heads=8, n_kv_heads=3), pm.ERR_INVALID_ARG), (dict(n_q_heads=0, n_kv_heads=1), pm.ERR_INVALID_ARG),
+    (dict(n_q_heads=8, n_kv_heads=2, head_dim=96), pm.ERR_UNSUPPORTED),
+    (dict(n_q_heads=8, n_kv_heads=2, page_tokens=48), pm.ERR_UNSUPPORTED),
+    (dict(n_q_heads=258, n_kv_heads=2), pm.ERR_UNSUPPORTED), (dict(n_q_heads=8192, n_kv_heads=8192), pm.ERR_UNSUPPORTED),
+    (dict(n_q_heads=8, n_kv_heads=2, softmax_scale=float("nan")), pm.ERR_INVALID_ARG),
+    (dict(n_q_heads=8, n_kv_heads=2, softmax_scale=float("inf")), pm.ERR_INVALID_ARG)])
+def test_config_refusals(args, status):
+    out = ctypes.c_size_t(0)
+    assert pm._lib.pnmix_kv4_cache_bytes(B(pm.KV4Config.make(**args)), 4, B(out)) == status
+    assert pm._lib.pnmix_kv4_workspace_bytes(B(pm.KV4Config.make(**args)), B(batch())) == 0
+
+
+BATCHES = [(dict(batch=0), pm.ERR_INVALID_ARG), (dict(n_tokens=-1), pm.ERR_INVALID_ARG),
+           (dict(max_pages=0), pm.ERR_INVALID_ARG), (dict(kv_len=None), pm.ERR_INVALID_ARG),
+           (dict(page_table=None), pm.ERR_INVALID_ARG), (dict(max_q=0), pm.ERR_INVALID_ARG),
+           (dict(max_q=7), pm.ERR_INVALID_ARG), (dict(batch=4097), pm.ERR_UNSUPPORTED),
+           (dict(max_pages=1 << 28), pm.ERR_UNSUPPORTED), (dict(n_tokens=1 << 28, max_q=9), pm.ERR_UNSUPPORTED),
+           (dict(q_start=None, n_tokens=7), pm.ERR_INVALID_ARG),
+           (dict(q_start=None, max_q=2), pm.ERR_INVALID_ARG),
+           (dict(kv_len=P + 2), pm.ERR_ALIGNMENT), (dict(q_start=P + 1), pm.ERR_ALIGNMENT)]
+
+
+@no_gpu
+@pytest.mark.parametrize("change,status", BATCHES)
+def test_batch_refusals(change, status):
+    cfg = pm.KV4Config.make(8, 2)
+    c, b, L = cache(cfg), batch(**change), pm._lib
+    k, q = rows(2), rows(8)
+    rope = pm.Rope.make(128)
+    ws = ctypes.c_void_p(P)
+    assert L.pnmix_kv4_append(B(cfg), B(b), B(k), B(k), B(c), None) == status
+    assert L.pnmix_kv4_append_qkv(B(cfg), B(rope), B(b), B(q), B(k), B(k), None, None, P, B(q), B(c), None) == status
+    assert L.pnmix_kv4_read(B(cfg), B(b), B(c), B(k), B(k), None) == status
+    assert L.pnmix_kv4_attention(B(cfg), B(b), B(q), B(c), B(q), ws, 1 << 40, None) == status
+    assert L.pnmix_kv4_workspace_bytes(B(cfg), B(b)) == 0
+
+
+ROWS = [(dict(data=None), pm.ERR_INVALID_ARG), (dict(data=P + 8), pm.ERR_ALIGNMENT), (dict(ts=1028), pm.ERR_ALIGNMENT),
+        (dict(hs=132), pm.ERR_ALIGNMENT), (dict(ts=-1024), pm.ERR_INVALID_ARG)]
+WRITES = [(dict(ts=0), pm.ERR_INVALID_ARG), (dict(hs=64), pm.ERR_INVALID_ARG), (dict(ts=512), pm.ERR_INVALID_ARG)]
+
+
+@no_gpu
+@pytest.mark.parametrize("change,status", ROWS + WRITES)
+def test_row_refusals(change, status):
+    cfg = pm.KV4Config.make(8, 8)
+    c, b, L = cache(cfg), batch(), pm._lib
+    good, bad = rows(), rows(**change)
+    rope = pm.Rope.make(128)
+    ws = ctypes.c_void_p(P)
+    big = 1 << 40
+    writes = [L.pnmix_kv4_read(B(cfg), B(b), B(c), B(bad), B(good), None),
+              L.pnmix_kv4_read(B(cfg), B(b), B(c), B(good), B(bad), None),
+              L.pnmix_kv4_attention(B(cfg), B(b), B(good), B(c), B(bad), ws, big, None),
+              L.pnmix_norm_rope(B(rope), 6, 8, 8, B(good), B(good), None, None, P, B(bad), B(good), None),
+              L.pnmix_norm_rope(B(rope), 6, 8, 8, B(good), B(good), None, None, P, B(good), B(bad), None),
+              L.pnmix_kv4_append_qkv(B(cfg), B(rope), B(b), B(good), B(good), B(good), None, None, P, B(bad), B(c), None)]
+    assert writes == [status] * 6
+    if (change, status) in WRITES:
+        return
+    reads = [L.pnmix_kv4_append(B(cfg), B(b), B(bad), B(good), B(c), None),
+             L.pnmix_kv4_append(B(cfg), B(b), B(good), B(bad), B(c), None),
+             L.pnmix_kv4_attention(B(cfg), B(b), B(bad), B(c), B(good), ws, big, None),
+             L.pnmix_norm_rope(B(rope), 6, 8, 8, B(bad), B(good), None, None, P, B(good), B(good), None),
+             L.pnmix_norm_rope(B(rope), 6, 8, 8, B(good), B(bad), None, None, P, B(good), B(good), None),
+             L.pnmix_kv4_append_qkv(B(cfg), B(rope), B(b), B(good), B(bad), B(good), None, None, P, B(good), B(c), None)]
+    assert reads == [status] * 6
+
+
+@no_gpu
+def test_workspace_cache_and_rope_refusals():
+    cfg = pm.KV4Config.make(8, 2)
+    c, b, L, q, k = cache(cfg), batch(), pm._lib, rows(8), rows(2)
+    need = L.pnmix_kv4_workspace_bytes(B(cfg), B(b))
+    assert need > 0
+    att = lambda ws, n: L.pnmix_kv4_attention(B(cfg), B(b), B(q), B(c), B(q), ws, n, None)  # noqa: E731
+    assert att(None, need) == pm.ERR_INVALID_ARG
+    assert att(ctypes.c_void_p(P + 16), need) == pm.ERR_ALIGNMENT
+    assert att(ctypes.c_void_p(P), need - 1) == pm.ERR_CAPACITY
+    other = cache(pm.KV4Config.make(8, 4))
+    assert L.pnmix_kv4_append(B(cfg), B(b), B(k), B(k), B(other), None) == pm.ERR_INVALID_ARG
+    assert L.pnmix_kv4_append(B(cfg), B(b), B(k), B(k), None, None) == pm.ERR_INVALID_ARG
+    assert L.pnmix_kv4_cache_reset(None, None) == pm.ERR_INVALID_ARG
+    rope = pm.Rope.make(64)      # not the cache's head size
+    assert L.pnmix_kv4_append_qkv(B(cfg), B(rope), B(b), B(q), B(k), B(k), None, None, P, B(q), B(c), None) \
+        == pm.ERR_INVALID_ARG
+
+    def nr(rope, n=6, hq=8, hk=2, pos=P, w=None):
+        return L.pnmix_norm_rope(B(rope), n, hq, hk, B(q), B(k), w, None, pos, B(q), B(k), None)
+    good = pm.Rope.make(128)
+    assert nr(good, pos=None) == pm.ERR_INVALID_ARG and nr(good, w=P + 2) == pm.ERR_ALIGNMENT
+    assert nr(good, n=-1) == pm.ERR_INVALID_ARG and nr(good, hq=0, hk=0) == pm.ERR_INVALID_ARG
+    assert nr(good, n=1 << 28) == pm.ERR_UNSUPPORTED
+    assert nr(good, n=0, pos=None) == pm.OK              # nothing to do
+    for change, status in [(dict(head_dim=96), pm.ERR_UNSUPPORTED), (dict(rot_dim=24), pm.ERR_UNSUPPORTED),
+                           (dict(rot_dim=144), pm.ERR_UNSUPPORTED), (dict(n_axes=0), pm.ERR_UNSUPPORTED),
+                           (dict(n_axes=5), pm.ERR_UNSUPPORTED), (dict(eps=-1.0), pm.ERR_INVALID_ARG),
+                           (dict(eps=float("nan")), pm.ERR_INVALID_ARG)]:
+        r = pm.Rope.make(128)
+        for name, value in change.items():
+            setattr(r, name, value)
+        assert nr(r) == status, change
+    r = pm.Rope.make(128)
+    r.axis[5] = 1
+    assert nr(r) == pm.ERR_INVALID_ARG
+    r = pm.Rope.make(128)
+    r.inv_freq[0] = float("inf")
+    assert nr(r) == pm.ERR_INVALID_ARG
+
+
+def test_python_refusals():
+    with pytest.raises(ValueError):
+        pm.Rope.make(128, 64, inv_freq=[1.0] * 20)
+    with pytest.raises(ValueError):
+        pm.Rope.make(128, axes=[0] * 63)
+    with pytest.raises(ValueError):
+        pm.Rope.make(64, axes=[4] * 32)
+    with pytest.raises(TypeError):
+        pm.KV4Batch(torch.ones(2, dtype=torch.int32), torch.zeros(2, 3, dtype=torch.int32), n_tokens=2)
+    with pytest.raises(TypeError):
+        pm.norm_rope(pm.Rope.make(64), torch.zeros(1, 1, 64), torch.zeros(1, 1, 64), torch.zeros(1, 1))
+    with pytest.raises(pm.PNMixError):
+        pm.kv4_cache_bytes(pm.KV4Config.make(8, 3), 4)
+
+
+# ---------------------------------------------------------------- the restatement itself
+
+def test_layout_is_a_bijection_and_round_trips():
+    for D in (64, 128):
+        p = ref.Pages(2, 2, D, 32)
+        for side in (0, 1):
+            seen = {p._code(side, t, ch) for t in range(16) for ch in range(D)}
+            lo = 10 * D * side
+            assert len(seen) == 16 * D and {b for b, _ in seen} == set(range(lo, lo + 8 * D))
+        r = np.random.default_rng(0)
+        rows_ = r.standard_normal((32, 2, D)).astype(np.float32)
+        c, s, z = ref.quantise(rows_)
+        for t in range(32):
+            p.put(1, t, t % 2, c[t], s[t], z[t])
+        for t in range(32):
+            assert np.array_equal(p.get(1, t, t % 2), ref.stand_for(c[t], s[t], z[t]))
+        k, v, cs = ref.dequant_all(p.raw, D)
+        assert np.array_equal(k[1, :, 4], ref.stand_for(c[4], s[4], z[4]).astype(np.float64).reshape(2, D)) or \
+            np.allclose(k[1, :, 4], ref.stand_for(c[4], s[4], z[4]), rtol=2.0 ** -23)
+        assert np.allclose(v[1, :, 5], ref.stand_for(c[5], s[5], z[5]), rtol=2.0 ** -23)
+
+
+def test_quantiser_error_is_half_a_step():
+    x = np.random.default_rng(1).standard_normal((50, 3, 128)).astype(np.float32) * 100
+    c, s, z = ref.quantise(x)
+    y = ref.stand_for(c, s, z).reshape(50, 3, 4, 32)
+    step = s.astype(np.float32)[..., None]
+    # half a step, the fp16 rounding of the zero point (2^-11 of it) and of the scale (15 * 2^-11)
+    tol = step / 2 + np.abs(z.astype(np.float32))[..., None] * 2.0 ** -11 + step * 15 * 2.0 ** -11
+    assert (np.abs(y - x.reshape(y.shape)) <= tol).all()
+    assert ref.quantise(np.full((1, 1, 32), 7.0))[0].max() == 0
+
+
+def test_bf16_rounding_of_the_restatement():
+    x = np.random.default_rng(2).standard_normal(1000) * 10.0 ** np.arange(-30, 30).repeat(17)[:1000]
+    want = torch.from_numpy(x).to(torch.bfloat16).float().numpy()
+    got = ref.bf16(x)
+    # torch rounds through fp32: they differ where that is a tie at most
+    assert (got != want).sum() <= 2
+    f = x.astype(np.float32)
+    assert np.array_equal(ref.bf16_from_f32(f), torch.from_numpy(f).to(torch.bfloat16).float().numpy())
