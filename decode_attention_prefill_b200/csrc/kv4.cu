@@ -52,8 +52,12 @@ pnmix_status check_batch(const pnmix_kv4_batch* b, const Geo& g, Batch* out) {
   if (!b || !b->kv_len || !b->page_table) return PNMIX_ERR_INVALID_ARG;
   if (b->batch <= 0 || b->n_tokens < 0 || b->max_pages <= 0) return PNMIX_ERR_INVALID_ARG;
   if (b->batch > kMaxBatch) return PNMIX_ERR_UNSUPPORTED;
-  if (static_cast<long long>(b->max_pages) << g.page_shift > 1 << 30) return PNMIX_ERR_UNSUPPORTED;
-  if (static_cast<long long>(b->n_tokens) * g.Hq > 1 << 30) return PNMIX_ERR_UNSUPPORTED;
+  if (static_cast<long long>(b->max_pages) << g.page_shift > 1 << 29) return PNMIX_ERR_UNSUPPORTED;
+  if (b->n_tokens > 1 << 28 || static_cast<long long>(b->n_tokens) * g.Hq > 1 << 30) return PNMIX_ERR_UNSUPPORTED;
+  // the attention numbers its work in 64 bits, times the CTAs: heads x row tiles x tokens
+  const double tiles = static_cast<double>(g.Hkv) * (b->batch + static_cast<double>(b->n_tokens) * g.G / 8);
+  if (tiles * (static_cast<double>(static_cast<long long>(b->max_pages) << g.page_shift) + b->n_tokens + 4096) > 0x1p51)
+    return PNMIX_ERR_UNSUPPORTED;
   if (b->n_tokens > 0 && (b->max_q < 1 || b->max_q > b->n_tokens)) return PNMIX_ERR_INVALID_ARG;
   if (!b->q_start && b->n_tokens % b->batch) return PNMIX_ERR_INVALID_ARG;
   if (!b->q_start && b->max_q < b->n_tokens / b->batch) return PNMIX_ERR_INVALID_ARG;

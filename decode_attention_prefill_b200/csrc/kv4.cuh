@@ -8,7 +8,7 @@ namespace pnmix {
 namespace kv4 {
 
 constexpr int kBlock = 16;           // tokens of a block, the unit of the layout
-constexpr int kMaxBatch = 4096;
+constexpr int kMaxBatch = 2048;
 constexpr float kLimit = 61440.0f;   // magnitudes are stored up to this
 
 // A validated configuration and cache, by value to the kernels.

@@ -2,15 +2,15 @@
 // cache.
 //
 // A UNIT is a tile of RT query rows of one (sequence b, KV head h): row r of the T * G rows is
-// token j = r / G of the sequence's new tokens, query head h * G + r % G.  A unit counts
-// `lead` items for its fixed cost and one item per ITEM tokens of the sequence.  Units are
-// numbered b-major, then h, then tile; their items are numbered in that order, X in total,
-// and CTA i of N takes [floor(i X / N), floor((i + 1) X / N)).  Every CTA works the numbers
-// out from q_start and kv_len itself (a block-wide prefix sum), so any mix of lengths is
-// balanced and the host needs to know none.  A piece of a unit that does not cover it whole
-// leaves a partial (m, l, O) per row in slot i + unit (the slots of a unit are contiguous and
-// disjoint from other units'), which the combine kernel merges; a CTA that has a unit to
-// itself writes its rows at once.
+// token j = r / G of the sequence's new tokens, query head h * G + r % G.  Its cost is counted
+// in tokens: `lead` for its fixed part, and an upper bound of what its last row sees, which
+// grows by ceil(RT / G) from one tile to the next.  Units are numbered b-major, then h, then
+// tile; their tokens are numbered in that order, X in total, and CTA i of N takes
+// [floor(i X / N), floor((i + 1) X / N)).  Every CTA works the numbers out from q_start and
+// kv_len itself (a block-wide prefix sum), so any mix of lengths is balanced and the host
+// needs to know none.  A CTA that has a unit to itself writes its rows at once.  A piece of a
+// unit that does not cover it leaves a partial (m, l, O) per row, and the merge kernel joins
+// them: only the first and the last piece of a CTA can be such, so two slots per CTA do.
 #pragma once
 
 #include "decode_frag.cuh"
@@ -25,8 +25,8 @@ struct UnitInfo {     // of a unit that several CTAs share; first < 0: nothing t
 };
 
 struct Work {
-  float* part;        // [slots][RT][D + 4]: m, l, -, -, O
-  UnitInfo* info;     // [units], each written by the CTA that holds the unit's first item
+  float* part;        // [2 N][RT][D + 4]: m, l, -, -, O
+  UnitInfo* info;     // [units], each written by the CTA that holds the unit's first token
   int* count;         // units
 };
 
@@ -38,32 +38,53 @@ __host__ __forceinline__ long long max_units(const Geo& g, const Batch& bt, int 
 }
 
 struct Piece {
-  int b, h, tile, unit;
-  int lo, hi;             // items of the unit past its lead, [lo, hi)
-  int first, last;        // CTAs that share the unit
+  int b, h, tile;
+  int lo, hi;             // counted tokens of the unit past its lead, [lo, hi)
+  bool whole;             // the unit is this piece
+  int slot;               // of the partial otherwise
   int start, T, len;      // rows and tokens of the sequence
 };
 
-__device__ __forceinline__ int cta_of_item(long long x, long long X, int N) {
+__device__ __forceinline__ int cta_of_token(long long x, long long X, int N) {
   return static_cast<int>(((x + 1) * N - 1) / X);
+}
+
+// Slot of CTA k's piece of a unit whose first piece is CTA `first`'s.
+__device__ __forceinline__ int slot_of(int k, int first) { return 2 * k + (k == first ? 1 : 0); }
+
+// What the units of a sequence cost: tile t counts base + t * step tokens, n tiles.
+struct SeqCost {
+  int n;
+  long long base, step;
+  __device__ __forceinline__ long long before(long long t) const { return t * base + step * (t * (t - 1) / 2); }
+};
+
+__device__ __forceinline__ SeqCost seq_cost(int G, int RT, int lead, int T, int len) {
+  const int rows = T * G;
+  SeqCost c;
+  c.n = (rows + RT - 1) / RT;
+  const int last = min(RT, rows) - 1;   // of the first tile
+  c.base = lead + (rows ? max(0, len - T + 1 + last / G) : 0);
+  c.step = (RT + G - 1) / G;
+  return c;
 }
 
 // Shared-memory bytes of the prefix sums.
 __host__ __device__ __forceinline__ size_t plan_bytes(int B) { return (static_cast<size_t>(B) + 1) * 12 + 4; }
 
-// Prefix sums over the sequences: items[b] and units[b] before sequence b.  All threads of
-// the CTA call it.  Row ranges that are out of order or out of the tensors could name more
-// rows than the workspace is made for, so with any of those there is no work at all.
+// Prefix sums over the sequences: cost[b] and units[b] before sequence b.  All threads of the
+// CTA call it.  Row ranges that are out of order or out of the tensors could name more rows
+// than the workspace is made for, so with any of those there is no work at all.
 template <int THREADS>
-__device__ __forceinline__ void build_plan(const Geo& g, const Batch& bt, int RT, int item, int lead,
-                                           long long* items, int* units, long long* tmp) {
+__device__ __forceinline__ void build_plan(const Geo& g, const Batch& bt, int RT, int lead, long long* cost,
+                                           int* units, long long* tmp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = THREADS / 32;
   long long carry_i = 0;
   int carry_u = 0;
   bool bad = false, bad_len = false;
-  for (int base = 0; base < bt.B; base += THREADS) {
-    const int b = base + tid;
+  for (int first = 0; first < bt.B; first += THREADS) {
+    const int b = first + tid;
     long long it = 0;
     int un = 0;
     if (b < bt.B) {
@@ -72,9 +93,9 @@ __device__ __forceinline__ void build_plan(const Geo& g, const Batch& bt, int RT
         bad = true;
         T = 0;
       }
-      const int len = seq_len(bt, g.page_shift, b, bad_len);
-      un = g.Hkv * ((T * g.G + RT - 1) / RT);
-      it = static_cast<long long>(un) * (lead + (len + item - 1) / item);
+      const SeqCost c = seq_cost(g.G, RT, lead, T, seq_len(bt, g.page_shift, b, bad_len));
+      un = g.Hkv * c.n;
+      it = g.Hkv * c.before(c.n);
     }
     long long si = it;
     int su = un;
@@ -105,70 +126,83 @@ __device__ __forceinline__ void build_plan(const Geo& g, const Batch& bt, int RT
       carry_u += wu;
     }
     if (b < bt.B) {
-      items[b] = off_i + si - it;
+      cost[b] = off_i + si - it;
       units[b] = off_u + su - un;
     }
     __syncthreads();
   }
   const bool none = __syncthreads_or(bad);
   if (tid == 0) {
-    items[bt.B] = none ? 0 : carry_i;
+    cost[bt.B] = none ? 0 : carry_i;
     units[bt.B] = none ? 0 : carry_u;
   }
   if ((bad || bad_len) && blockIdx.x == 0) raise(g.error, PNMIX_DEVERR_BATCH);
   __syncthreads();
 }
 
-// Calls fn(piece) for every piece of this CTA, in order; uniform across the CTA.
+// Calls fn(piece) for every piece of this CTA, in order, until it returns false.  `writer`:
+// the one thread that notes the units for the merge.
 template <typename F>
-__device__ __forceinline__ void for_each_piece(const Geo& g, const Batch& bt, int RT, int item, int lead,
-                                               const long long* items, const int* units, const Work& wk, int grid,
-                                               F&& fn) {
-  const long long X = items[bt.B];
+__device__ __forceinline__ void for_each_piece(const Geo& g, const Batch& bt, int RT, int lead,
+                                               const long long* cost, const int* units, const Work& wk, int grid,
+                                               bool writer, F&& fn) {
+  const long long X = cost[bt.B];
   const int N = X < grid ? static_cast<int>(X) : grid, i = blockIdx.x;
-  if (i == 0 && threadIdx.x == 0) *wk.count = units[bt.B];
+  if (i == 0 && writer) *wk.count = units[bt.B];
   if (i >= N) return;
   long long x = X * i / N;
   const long long e = X * (i + 1) / N;
-  int lo = 0, hi = bt.B - 1;   // the sequence that holds item x: the last b with items[b] <= x
+  int lo = 0, hi = bt.B - 1;   // the sequence that holds token x: the last b with cost[b] <= x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (items[mid] <= x) lo = mid;
+    if (cost[mid] <= x) lo = mid;
     else hi = mid - 1;
   }
   int b = lo;
   while (x < e) {
-    while (items[b + 1] <= x) ++b;   // sequences without rows hold no items
+    while (cost[b + 1] <= x) ++b;   // sequences without rows cost nothing
     bool bad = false;
     Piece p;
     p.b = b;
     seq_rows(bt, b, p.start, p.T);
     p.len = seq_len(bt, g.page_shift, b, bad);
-    const long long per = lead + (p.len + item - 1) / item;
-    const int tiles = (p.T * g.G + RT - 1) / RT;
-    const int u = static_cast<int>((x - items[b]) / per);
-    const long long ustart = items[b] + u * per, uend = ustart + per;
+    const SeqCost c = seq_cost(g.G, RT, lead, p.T, p.len);
+    const long long head = c.before(c.n);
+    p.h = static_cast<int>((x - cost[b]) / head);
+    const long long hstart = cost[b] + p.h * head;
+    int t0 = 0, t1 = c.n - 1;     // the last tile that starts at or before x
+    while (t0 < t1) {
+      const int mid = (t0 + t1 + 1) >> 1;
+      if (hstart + c.before(mid) <= x) t0 = mid;
+      else t1 = mid - 1;
+    }
+    p.tile = t0;
+    const long long ustart = hstart + c.before(t0), uend = hstart + c.before(t0 + 1);
     const long long xe = uend < e ? uend : e;
-    p.h = u / tiles;
-    p.tile = u - p.h * tiles;
-    p.unit = units[b] + u;
+    const int first = cta_of_token(ustart, X, N), last = cta_of_token(uend - 1, X, N);
     p.lo = static_cast<int>(max(x - ustart - lead, 0ll));
     p.hi = static_cast<int>(max(xe - ustart - lead, 0ll));
-    p.first = cta_of_item(ustart, X, N);
-    p.last = cta_of_item(uend - 1, X, N);
-    if (threadIdx.x == 0 && x == ustart) {
+    p.whole = first == last;
+    p.slot = slot_of(i, first);
+    if (writer && x == ustart) {
       UnitInfo f;
-      f.first = p.first == p.last ? -1 : p.first;
-      f.last = p.last;
+      f.first = p.whole ? -1 : first;
+      f.last = last;
       f.b = p.b;
       f.h = p.h;
       f.tile = p.tile;
-      wk.info[p.unit] = f;
+      wk.info[units[b] + p.h * c.n + p.tile] = f;
     }
-    fn(p);
+    if (!fn(p)) return;
     x = xe;
   }
 }
+
+constexpr int kMaxChunkCtas = 160;   // one per SM
+
+// kv4_chunk.cu; rt 128 or 256 rows per unit.
+cudaError_t launch_chunk(const Geo& g, const Batch& bt, const Rows& q, const pnmix_rows& out, const Work& wk, int rt,
+                         cudaStream_t s);
 
 }  // namespace kv4
 }  // namespace pnmix

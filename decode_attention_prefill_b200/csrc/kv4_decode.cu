@@ -93,15 +93,15 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
   float* merge = reinterpret_cast<float*>(smem);           // [kWarps][RT][kStride], after the ring's use
   __shared__ uint64_t bars[kWarps][kStages];
   __shared__ long long tmp[2 * kWarps];
-  long long* items = reinterpret_cast<long long*>(smem + kWarps * kStages * kStageBytes);
-  int* units = reinterpret_cast<int*>(items + bt.B + 1);
+  long long* cost = reinterpret_cast<long long*>(smem + kWarps * kStages * kStageBytes);
+  int* units = reinterpret_cast<int*>(cost + bt.B + 1);
   uint64_t* full = bars[warp];
   if (lane == 0) {
     for (int k = 0; k < kStages; ++k) mbar_init(full + k, 1);
     fence_mbar_init();
   }
   asm volatile("griddepcontrol.launch_dependents;");
-  build_plan<kThreads>(g, bt, RT, kStageTok, a.lead, items, units, tmp);
+  build_plan<kThreads>(g, bt, RT, a.lead, cost, units, tmp);
 
   // tokens of this lane inside a block: A rows gq and gq + 8 (keys), tq's four (values)
   const int r0 = (gq & 1) ? 7 - (gq >> 1) : gq >> 1;
@@ -113,14 +113,15 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
   uint32_t nis = 0, ncons = 0;   // stages this warp issued and consumed
   bool dead = false;             // a staging wait ran out
 
-  for_each_piece(g, bt, RT, kStageTok, a.lead, items, units, a.wk, gridDim.x, [&](const Piece& pc) {
+  for_each_piece(g, bt, RT, a.lead, cost, units, a.wk, gridDim.x, tid == 0, [&](const Piece& pc) -> bool {
     const int row_first = pc.tile * RT, nrows = min(RT, pc.T * g.G - row_first);
     // tokens that row r sees, and the tile's most
     const int base_seen = pc.len - pc.T + 1;
     const int tile_seen = max(0, base_seen + (row_first + nrows - 1) / g.G);
     const int least_seen = base_seen + row_first / g.G;
     const int nstage = (tile_seen + kStageTok - 1) / kStageTok;
-    const int p_lo = min(pc.lo, nstage), p_hi = min(pc.hi, nstage);
+    const int p_lo = min((pc.lo + kStageTok - 1) / kStageTok, nstage);   // the stages that start in [lo, hi)
+    const int p_hi = min((pc.hi + kStageTok - 1) / kStageTok, nstage);
     const int per = (p_hi - p_lo + kWarps - 1) / kWarps;
     const int s_lo = min(p_lo + warp * per, p_hi), s_hi = min(s_lo + per, p_hi);
 
@@ -447,7 +448,6 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
         }
       }
     __syncthreads();
-    const bool whole = pc.first == pc.last;
     for (int i = tid; i < nrows * (D / 4); i += kThreads) {
       const int v = i / (D / 4), c4 = i - v * (D / 4);
       float m = -1e30f, l = 0.f;
@@ -472,7 +472,7 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
           o.w = fmaf(r.w, w[k], o.w);
         }
       }
-      if (whole) {
+      if (pc.whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int row = row_first + v, j = row / g.G, hg = row - j * g.G;
         const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
@@ -483,12 +483,13 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
         *reinterpret_cast<uint2*>(a.out + static_cast<long long>(pc.start + j) * a.out_ts +
                                   (pc.h * g.G + hg) * a.out_hs + 4 * c4) = pk;
       } else {
-        float* part = a.wk.part + (static_cast<size_t>(blockIdx.x + pc.unit) * RT + v) * kStride;
+        float* part = a.wk.part + (static_cast<size_t>(pc.slot) * RT + v) * kStride;
         if (c4 == 0) *reinterpret_cast<float2*>(part) = make_float2(m, l);
         *reinterpret_cast<float4*>(part + 4 + 4 * c4) = o;
       }
     }
     __syncthreads();
+    return true;
   });
 }
 
@@ -506,12 +507,13 @@ merge_kernel(const __grid_constant__ AttnArgs a, int RT) {
   int start, T;
   seq_rows(a.bt, f.b, start, T);
   const int nrows = min(RT, T * a.g.G - f.tile * RT), n = f.last - f.first + 1;
-  const size_t step = static_cast<size_t>(RT) * kStride;
+  const size_t slot_floats = static_cast<size_t>(RT) * kStride;
   for (int v = blockIdx.y * kWarps + warp; v < nrows; v += kWarps * gridDim.y) {
-    const float* base = a.wk.part + (static_cast<size_t>(f.first + unit) * RT + v) * kStride;
+    const float* base = a.wk.part + static_cast<size_t>(v) * kStride;
+    auto partial = [&](int k) { return base + slot_of(f.first + k, f.first) * slot_floats; };
     float m = -1e30f;
     for (int k = lane; k < n; k += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(base + k * step);
+      const float2 ml = *reinterpret_cast<const float2*>(partial(k));
       if (ml.y != 0.f) m = fmaxf(m, ml.x);
     }
 #pragma unroll
@@ -521,14 +523,14 @@ merge_kernel(const __grid_constant__ AttnArgs a, int RT) {
     for (int i = 0; i < C; ++i) o[i] = 0.f;
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
-      const float2 ml = *reinterpret_cast<const float2*>(base + k * step);
+      const float2 ml = *reinterpret_cast<const float2*>(partial(k));
       const float w = ml.y == 0.f ? 0.f : ex2(ml.x - m);
       float r[C];
       if constexpr (C == 4) {
-        const float4 t = *reinterpret_cast<const float4*>(base + k * step + 4 + 4 * lane);
+        const float4 t = *reinterpret_cast<const float4*>(partial(k) + 4 + 4 * lane);
         r[0] = t.x; r[1] = t.y; r[2] = t.z; r[3] = t.w;
       } else {
-        const float2 t = *reinterpret_cast<const float2*>(base + k * step + 4 + 2 * lane);
+        const float2 t = *reinterpret_cast<const float2*>(partial(k) + 4 + 2 * lane);
         r[0] = t.x; r[1] = t.y;
       }
       l = fmaf(ml.y, w, l);
@@ -573,27 +575,44 @@ constexpr int kMaxCtas = 1024;
 
 }  // namespace
 
-static int tile_rows(const Geo& g, const Batch& bt) { return g.G * bt.max_q <= 8 ? 8 : 16; }
-
-size_t attention_workspace_bytes(const Geo& g, const Batch& bt) {
-  const int rt = tile_rows(g, bt);
-  const long long units = max_units(g, bt, rt);
-  return 256 + (units * sizeof(UnitInfo) + 255) / 256 * 256 +
-         static_cast<size_t>(kMaxCtas + units) * rt * part_stride(g.D) * sizeof(float);
+// Query rows of a unit.  Up to 8 or 16 rows of a sequence and KV head take the kernel above,
+// more the tcgen05 one.
+static int tile_rows(const Geo& g, const Batch& bt) {
+  const int rows = g.G * bt.max_q;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
 }
 
+struct WorkLayout {
+  long long units;
+  size_t info, part, total;
+};
+
+static WorkLayout work_layout(const Geo& g, const Batch& bt, int rt) {
+  WorkLayout w;
+  w.units = max_units(g, bt, rt);
+  w.info = 256;
+  w.part = w.info + (w.units * sizeof(UnitInfo) + 255) / 256 * 256;
+  w.total = w.part + 2 * static_cast<size_t>(rt > 16 ? kMaxChunkCtas : kMaxCtas) * rt * part_stride(g.D) * sizeof(float);
+  return w;
+}
+
+size_t attention_workspace_bytes(const Geo& g, const Batch& bt) { return work_layout(g, bt, tile_rows(g, bt)).total; }
+
 template <int D, int NT>
-static cudaError_t launch_rows(AttnArgs& a, long long units, cudaStream_t s) {
+static cudaError_t launch_rows(AttnArgs& a, cudaStream_t s) {
   const size_t smem = kWarps * kStages * 40 * D + plan_bytes(a.bt.B);
   int wave = 0;
-  cudaError_t e = wave_of<D, NT>(smem, &wave);
+  const cudaError_t e = wave_of<D, NT>(smem, &wave);
   if (e != cudaSuccess) return e;
-  if (wave > kMaxCtas) wave = kMaxCtas;
-  decode_kernel<D, NT><<<wave, kThreads, smem, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  decode_kernel<D, NT><<<wave < kMaxCtas ? wave : kMaxCtas, kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_merge(const AttnArgs& a, long long units, int rt, cudaStream_t s) {
   // the merge is resident early and waits for the partials (griddepcontrol)
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units), NT == 1 ? 1 : 2);
+  cfg.gridDim = dim3(static_cast<unsigned>(units), rt == 8 ? 1 : rt == 16 ? 2 : 8);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr;
@@ -601,13 +620,13 @@ static cudaError_t launch_rows(AttnArgs& a, long long units, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, a, 8 * NT);
+  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, a, rt);
 }
 
 cudaError_t launch_attention(const Geo& g, const Batch& bt, const pnmix_rows& q, const pnmix_rows& out, void* ws,
                              cudaStream_t s) {
   const int rt = tile_rows(g, bt);
-  const long long units = max_units(g, bt, rt);
+  const WorkLayout w = work_layout(g, bt, rt);
   AttnArgs a{};
   a.g = g;
   a.bt = bt;
@@ -615,13 +634,20 @@ cudaError_t launch_attention(const Geo& g, const Batch& bt, const pnmix_rows& q,
   a.out = out.data;
   a.out_ts = out.token_stride;
   a.out_hs = out.head_stride;
-  a.lead = 12;
-  char* w = static_cast<char*>(ws);
-  a.wk.count = reinterpret_cast<int*>(w);
-  a.wk.info = reinterpret_cast<UnitInfo*>(w + 256);
-  a.wk.part = reinterpret_cast<float*>(w + 256 + (units * sizeof(UnitInfo) + 255) / 256 * 256);
-  if (g.D == 64) return rt == 8 ? launch_rows<64, 1>(a, units, s) : launch_rows<64, 2>(a, units, s);
-  return rt == 8 ? launch_rows<128, 1>(a, units, s) : launch_rows<128, 2>(a, units, s);
+  a.lead = 384;
+  char* base = static_cast<char*>(ws);
+  a.wk.count = reinterpret_cast<int*>(base);
+  a.wk.info = reinterpret_cast<UnitInfo*>(base + w.info);
+  a.wk.part = reinterpret_cast<float*>(base + w.part);
+  cudaError_t e;
+  if (rt > 16)
+    e = launch_chunk(g, bt, a.q, out, a.wk, rt, s);
+  else if (g.D == 64)
+    e = rt == 8 ? launch_rows<64, 1>(a, s) : launch_rows<64, 2>(a, s);
+  else
+    e = rt == 8 ? launch_rows<128, 1>(a, s) : launch_rows<128, 2>(a, s);
+  if (e != cudaSuccess) return e;
+  return g.D == 64 ? launch_merge<64>(a, w.units, rt, s) : launch_merge<128>(a, w.units, rt, s);
 }
 
 }  // namespace kv4

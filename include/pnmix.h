@@ -600,7 +600,7 @@ typedef struct {
  * padding or find them another place.
  */
 typedef struct {
-  int32_t batch;              /* 1 .. 4096 */
+  int32_t batch;              /* 1 .. 2048 */
   int32_t n_tokens;           /* rows of the token tensors, >= q_start[batch] */
   int32_t max_pages;          /* entries of a row of page_table */
   int32_t max_q;              /* no sequence has more rows than this (1 .. n_tokens) */

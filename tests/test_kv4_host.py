@@ -68,7 +68,7 @@ def test_config_refusals(args, status):
 BATCHES = [(dict(batch=0), pm.ERR_INVALID_ARG), (dict(n_tokens=-1), pm.ERR_INVALID_ARG),
            (dict(max_pages=0), pm.ERR_INVALID_ARG), (dict(kv_len=None), pm.ERR_INVALID_ARG),
            (dict(page_table=None), pm.ERR_INVALID_ARG), (dict(max_q=0), pm.ERR_INVALID_ARG),
-           (dict(max_q=7), pm.ERR_INVALID_ARG), (dict(batch=4097), pm.ERR_UNSUPPORTED),
+           (dict(max_q=7), pm.ERR_INVALID_ARG), (dict(batch=2049), pm.ERR_UNSUPPORTED),
            (dict(max_pages=1 << 28), pm.ERR_UNSUPPORTED), (dict(n_tokens=1 << 28, max_q=9), pm.ERR_UNSUPPORTED),
            (dict(q_start=None, n_tokens=7), pm.ERR_INVALID_ARG),
            (dict(q_start=None, max_q=2), pm.ERR_INVALID_ARG),
