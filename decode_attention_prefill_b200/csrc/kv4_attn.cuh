@@ -3,14 +3,16 @@
 //
 // A UNIT is a tile of RT query rows of one (sequence b, KV head h): row r of the T * G rows is
 // token j = r / G of the sequence's new tokens, query head h * G + r % G.  Its cost is counted
-// in tokens: `lead` for its fixed part, and an upper bound of what its last row sees, which
-// grows by ceil(RT / G) from one tile to the next.  Units are numbered b-major, then h, then
-// tile; their tokens are numbered in that order, X in total, and CTA i of N takes
-// [floor(i X / N), floor((i + 1) X / N)).  Every CTA works the numbers out from q_start and
+// in tokens: `lead` for its fixed part (at most a quarter of what a CTA gets), and an upper
+// bound of what its last row sees, which grows by ceil(RT / G) from one tile to the next.
+// Units are numbered b-major, then h, then tile; their tokens are numbered in that order, X in
+// total, and CTA i of N takes [floor(i X / N), floor((i + 1) X / N)), N as many as the GPU holds
+// but none with less than `slice` tokens.  Every CTA works the numbers out from q_start and
 // kv_len itself (a block-wide prefix sum), so any mix of lengths is balanced and the host
 // needs to know none.  A CTA that has a unit to itself writes its rows at once.  A piece of a
 // unit that does not cover it leaves a partial (m, l, O) per row, and the merge kernel joins
-// them: only the first and the last piece of a CTA can be such, so two slots per CTA do.
+// them.  Only the first and the last piece of a CTA can be such, so two slots per CTA do, and
+// at most one shared unit begins in a CTA, which notes it.
 #pragma once
 
 #include "decode_frag.cuh"
@@ -19,22 +21,25 @@
 namespace pnmix {
 namespace kv4 {
 
-struct UnitInfo {     // of a unit that several CTAs share; first < 0: nothing to merge
-  int first, last;    // CTAs
-  int b, h, tile, pad[3];
+struct UnitInfo {     // of the unit that begins in a CTA and ends in `last`; last < 0: there is none
+  int last, b, h, tile;
 };
 
 struct Work {
-  float* part;        // [2 N][RT][D + 4]: m, l, -, -, O
-  UnitInfo* info;     // [units], each written by the CTA that holds the unit's first token
-  int* count;         // units
+  float* part;        // [2 N] slots, part_floats each
+  UnitInfo* info;     // [N]
 };
 
-__host__ __device__ __forceinline__ int part_stride(int D) { return D + 4; }
+// Tokens of a unit's fixed cost, and the fewest a CTA is started for.
+struct Grain {
+  int lead, slice;
+};
 
-// Host bound of the number of units: sum over b of Hkv * ceil(G T_b / RT).
-__host__ __forceinline__ long long max_units(const Geo& g, const Batch& bt, int rt) {
-  return static_cast<long long>(g.Hkv) * (bt.B + static_cast<long long>(bt.n_tokens) * g.G / rt);
+// A slot: (m, l) per row, then O as [D / 4][RT][4], so that a warp of rows writes it coalesced.
+__host__ __device__ __forceinline__ size_t part_floats(int D, int rt) { return static_cast<size_t>(rt) * (D + 2); }
+template <int D>
+__device__ __forceinline__ float* part_of(float* part, int slot, int rt) {
+  return part + slot * part_floats(D, rt);
 }
 
 struct Piece {
@@ -55,29 +60,43 @@ __device__ __forceinline__ int slot_of(int k, int first) { return 2 * k + (k == 
 // What the units of a sequence cost: tile t counts base + t * step tokens, n tiles.
 struct SeqCost {
   int n;
-  long long base, step;
+  long long base, step;    // base without the lead
   __device__ __forceinline__ long long before(long long t) const { return t * base + step * (t * (t - 1) / 2); }
 };
 
-__device__ __forceinline__ SeqCost seq_cost(int G, int RT, int lead, int T, int len) {
+__device__ __forceinline__ SeqCost seq_cost(int G, int RT, int T, int len) {
   const int rows = T * G;
   SeqCost c;
   c.n = (rows + RT - 1) / RT;
   const int last = min(RT, rows) - 1;   // of the first tile
-  c.base = lead + (rows ? max(0, len - T + 1 + last / G) : 0);
+  c.base = rows ? max(0, len - T + 1 + last / G) : 0;
   c.step = (RT + G - 1) / G;
   return c;
 }
 
-// Shared-memory bytes of the prefix sums.
-__host__ __device__ __forceinline__ size_t plan_bytes(int B) { return (static_cast<size_t>(B) + 1) * 12 + 4; }
+// The numbers of a launch: this, then the tokens and the units before each sequence.
+struct Plan {
+  long long X;      // tokens in all, the leads included
+  int lead, N;
+  __device__ __forceinline__ const long long* tokens() const { return reinterpret_cast<const long long*>(this + 1); }
+  __device__ __forceinline__ long long before(int b, int B) const {
+    const int* units = reinterpret_cast<const int*>(tokens() + B + 1);
+    return tokens()[b] + static_cast<long long>(units[b]) * lead;
+  }
+};
+__host__ __device__ __forceinline__ size_t plan_bytes(int B) {
+  return (sizeof(Plan) + (static_cast<size_t>(B) + 1) * 12 + 15) / 16 * 16;
+}
 
-// Prefix sums over the sequences: cost[b] and units[b] before sequence b.  All threads of the
-// CTA call it.  Row ranges that are out of order or out of the tensors could name more rows
+// All threads of the CTA call it, `at` plan_bytes of its own, `tmp` shared memory, two words per
+// warp.  Row ranges that are out of order or out of the tensors could name more rows
 // than the workspace is made for, so with any of those there is no work at all.
 template <int THREADS>
-__device__ __forceinline__ void build_plan(const Geo& g, const Batch& bt, int RT, int lead, long long* cost,
-                                           int* units, long long* tmp) {
+__device__ __forceinline__ const Plan& build_plan(const Geo& g, const Batch& bt, int RT, const Grain& grain, void* at,
+                                                  long long* tmp) {
+  Plan* plan = static_cast<Plan*>(at);
+  long long* tokens = reinterpret_cast<long long*>(plan + 1);
+  int* units = reinterpret_cast<int*>(tokens + bt.B + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = THREADS / 32;
   long long carry_i = 0;
@@ -93,7 +112,7 @@ __device__ __forceinline__ void build_plan(const Geo& g, const Batch& bt, int RT
         bad = true;
         T = 0;
       }
-      const SeqCost c = seq_cost(g.G, RT, lead, T, seq_len(bt, g.page_shift, b, bad_len));
+      const SeqCost c = seq_cost(g.G, RT, T, seq_len(bt, g.page_shift, b, bad_len));
       un = g.Hkv * c.n;
       it = g.Hkv * c.before(c.n);
     }
@@ -126,50 +145,66 @@ __device__ __forceinline__ void build_plan(const Geo& g, const Batch& bt, int RT
       carry_u += wu;
     }
     if (b < bt.B) {
-      cost[b] = off_i + si - it;
+      tokens[b] = off_i + si - it;
       units[b] = off_u + su - un;
     }
     __syncthreads();
   }
   const bool none = __syncthreads_or(bad);
+  if (none) carry_i = carry_u = 0;
   if (tid == 0) {
-    cost[bt.B] = none ? 0 : carry_i;
-    units[bt.B] = none ? 0 : carry_u;
+    tokens[bt.B] = carry_i;
+    units[bt.B] = carry_u;
+    const int lead =
+        static_cast<int>(min(max(carry_i / (4 * gridDim.x), 16ll), static_cast<long long>(grain.lead)));
+    const long long X = carry_i + static_cast<long long>(carry_u) * lead;
+    plan->lead = lead;
+    plan->X = X;
+    plan->N = static_cast<int>(min(max(X / grain.slice, X > 0 ? 1ll : 0ll), static_cast<long long>(gridDim.x)));
   }
   if ((bad || bad_len) && blockIdx.x == 0) raise(g.error, PNMIX_DEVERR_BATCH);
   __syncthreads();
+  return *plan;
 }
 
-// Calls fn(piece) for every piece of this CTA, in order, until it returns false.  `writer`:
-// the one thread that notes the units for the merge.
-template <typename F>
-__device__ __forceinline__ void for_each_piece(const Geo& g, const Batch& bt, int RT, int lead,
-                                               const long long* cost, const int* units, const Work& wk, int grid,
-                                               bool writer, F&& fn) {
-  const long long X = cost[bt.B];
-  const int N = X < grid ? static_cast<int>(X) : grid, i = blockIdx.x;
-  if (i == 0 && writer) *wk.count = units[bt.B];
-  if (i >= N) return;
-  long long x = X * i / N;
-  const long long e = X * (i + 1) / N;
-  int lo = 0, hi = bt.B - 1;   // the sequence that holds token x: the last b with cost[b] <= x
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cost[mid] <= x) lo = mid;
-    else hi = mid - 1;
-  }
-  int b = lo;
-  while (x < e) {
-    while (cost[b + 1] <= x) ++b;   // sequences without rows cost nothing
+// Calls fn(piece) for every piece of this CTA, in order, until it returns false.  The piece and
+// where to go on lie in shared memory (`at`, of the calling warp), so that they hold no
+// registers while fn works.  SOLO: one lane calls it, else a whole warp.  `writer`: the one
+// thread that notes the shared unit for the merge.
+struct PieceSlot {
+  Piece p;
+  long long next;
+};
+
+template <bool SOLO, typename F>
+__device__ __forceinline__ void for_each_piece(const Geo& g, const Batch& bt, int RT, const Plan& plan, const Work& wk,
+                                               PieceSlot* at, bool writer, F&& fn) {
+  if (writer) wk.info[blockIdx.x].last = -1;
+  if (static_cast<int>(blockIdx.x) >= plan.N) return;
+  const bool scribe = SOLO || (threadIdx.x & 31) == 0;
+  if (scribe) at->next = plan.X * blockIdx.x / plan.N;
+  while (true) {
+    if (!SOLO) __syncwarp();
+    const long long X = plan.X, x = at->next;
+    const int N = plan.N, lead = plan.lead;
+    const long long e = X * (blockIdx.x + 1) / N;
+    if (x >= e) return;
+    int lo = 0, hi = bt.B - 1;   // the sequence that holds token x: the last that starts at or before it
+    while (lo < hi) {            // (and holds tokens: empty ones start where the next does)
+      const int mid = (lo + hi + 1) >> 1;
+      if (plan.before(mid, bt.B) <= x) lo = mid;
+      else hi = mid - 1;
+    }
     bool bad = false;
     Piece p;
-    p.b = b;
-    seq_rows(bt, b, p.start, p.T);
-    p.len = seq_len(bt, g.page_shift, b, bad);
-    const SeqCost c = seq_cost(g.G, RT, lead, p.T, p.len);
-    const long long head = c.before(c.n);
-    p.h = static_cast<int>((x - cost[b]) / head);
-    const long long hstart = cost[b] + p.h * head;
+    p.b = lo;
+    seq_rows(bt, lo, p.start, p.T);
+    p.len = seq_len(bt, g.page_shift, lo, bad);
+    SeqCost c = seq_cost(g.G, RT, p.T, p.len);
+    c.base += lead;
+    const long long head = c.before(c.n), seq = plan.before(lo, bt.B);
+    p.h = static_cast<int>((x - seq) / head);
+    const long long hstart = seq + p.h * head;
     int t0 = 0, t1 = c.n - 1;     // the last tile that starts at or before x
     while (t0 < t1) {
       const int mid = (t0 + t1 + 1) >> 1;
@@ -183,26 +218,24 @@ __device__ __forceinline__ void for_each_piece(const Geo& g, const Batch& bt, in
     p.lo = static_cast<int>(max(x - ustart - lead, 0ll));
     p.hi = static_cast<int>(max(xe - ustart - lead, 0ll));
     p.whole = first == last;
-    p.slot = slot_of(i, first);
-    if (writer && x == ustart) {
-      UnitInfo f;
-      f.first = p.whole ? -1 : first;
-      f.last = last;
-      f.b = p.b;
-      f.h = p.h;
-      f.tile = p.tile;
-      wk.info[units[b] + p.h * c.n + p.tile] = f;
+    p.slot = slot_of(blockIdx.x, first);
+    if (writer && x == ustart && !p.whole) wk.info[blockIdx.x] = {last, p.b, p.h, p.tile};
+    if (!SOLO) __syncwarp();      // every lane has read the last piece and `next`
+    if (scribe) {
+      at->p = p;
+      at->next = xe;
     }
-    if (!fn(p)) return;
-    x = xe;
+    if (!SOLO) __syncwarp();
+    if (!fn(at->p)) return;
   }
 }
 
 constexpr int kMaxChunkCtas = 160;   // one per SM
 
-// kv4_chunk.cu; rt 128 or 256 rows per unit.
-cudaError_t launch_chunk(const Geo& g, const Batch& bt, const Rows& q, const pnmix_rows& out, const Work& wk, int rt,
-                         cudaStream_t s);
+// kv4_chunk.cu; rt 128 or 256 rows per unit; plans: kMaxChunkCtas x plan_bytes of the
+// workspace, 8-byte aligned.  *ctas: the launch's.
+cudaError_t launch_chunk(const Geo& g, const Batch& bt, const Rows& q, const pnmix_rows& out, const Work& wk,
+                         uint8_t* plans, int rt, int* ctas, cudaStream_t s);
 
 }  // namespace kv4
 }  // namespace pnmix

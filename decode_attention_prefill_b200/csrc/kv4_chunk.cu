@@ -5,23 +5,29 @@
 // they can be kept fed; next to them stand one exp2 per row and token (16 a cycle per SM: as
 // long as both products of 128 x 128 x 128 take) and the shared-memory reads of the operands.
 // So one CTA per SM holds two STREAMS whose softmax and products alternate, and everything
-// around them has warps of its own (18 warps):
+// around them has warps of its own (19 warps, 96 registers a thread):
 //   warps 0..3, 4..7   softmax of stream 0 and 1: a thread owns a row (a TMEM lane)
 //   warps 8..11        write the key tile: 128 tokens x head_dim, fp16(code * s + z)
 //   warps 12..15       write the value tile: head_dim x 128 tokens, fp16(code * s + z)
 //   warp 16            one thread issues the products (tcgen05.mma, accumulators in TMEM)
 //   warp 17            stages the packed pages by bulk copies (8 blocks of 16 tokens a tile)
+//   warp 18            works out the CTA's pieces of work, one ahead of the others
 // With more than 128 rows per unit the streams are two tiles of 128 query rows, and both meet
 // every key and value tile (its unpacking is then paid once per 256 rows); with up to 128 rows
 // they are the same rows over the even and the odd tiles, and their sums are joined at the end.
 //
 //   S = Q K^T   A = query rows (fp16, scaled by a power of two per row so that bf16 channels
 //               are exact), B = key tile, both from shared memory; fp32 in TMEM
-//   softmax     row maximum of the tile (one pass over S in TMEM), a reference that moves only
-//               when a logit would give p above 2^14 (then the row of O is rescaled in TMEM),
-//               p = 2^(x - m) rounded to fp16 (2^-12 of each weight at most) over the S it came
-//               from, the denominator summed in fp32
+//   softmax     one pass over S in TMEM, 32 columns at a time: p = 2^(x - m), summed in fp32
+//               and rounded to fp16 (2^-12 of each weight at most) over the S it came from.  The
+//               reference m moves only when a row's sum of 32 passes 2^15 (so no p is above the
+//               fp16 range, and no maximum has to be taken otherwise); what the row has so far,
+//               in TMEM and out of it, is then rescaled by a power of two
 //   O += P V    A = P from TMEM, B = value tile
+// What every role runs once per piece is kept short: straight-line code that is met cold costs
+// about ten cycles an instruction here (five roles share the instruction cache), and a spilled
+// register costs an access to L2 (the shared memory takes the whole of L1).
+//
 // The operands lie in shared memory in the K-major form without swizzle: 8-row pieces of 8 x 16
 // bytes.  The order of the channels inside K (keys and queries alike) and of the value rows is
 // free; it is chosen so that code words unpack without moving codes between lanes and 16-byte
@@ -35,10 +41,10 @@ namespace pnmix {
 namespace kv4 {
 namespace {
 
-constexpr int kThreads = 576;
+constexpr int kThreads = 608;
 constexpr int kTile = 128;                  // tokens of a key / value tile; rows of a stream
 constexpr uint32_t kCommitLimit = 1u << 22; // try_wait rounds of a wait inside the CTA
-constexpr float kSlack = 14.f;              // log2 of the largest p before the reference moves
+constexpr float kTop = 32768.f;             // largest sum of 32 weights before the reference moves
 constexpr int kTmemO = 256;                 // TMEM columns: S (and P) of stream s at 128 s, O at 256 + 128 s
 
 // ---- tcgen05
@@ -82,37 +88,22 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// 32 consecutive columns of this thread's TMEM lane (warp-collective).
-__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(at)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_st32(uint32_t at, const float (&v)[32]) {
+// Consecutive columns of this thread's TMEM lane (warp-collective).
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
       "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(at), "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-        "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-        "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
-        "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
-        "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
-        "r"(__float_as_uint(v[15])), "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])),
-        "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])), "r"(__float_as_uint(v[20])),
-        "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
-        "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])),
-        "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])),
-        "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
+      ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+        "r"(v[3]), "r"(v[4]), "r"(v[5]),
+        "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]),
+        "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15]), "r"(v[16]), "r"(v[17]),
+        "r"(v[18]), "r"(v[19]), "r"(v[20]),
+        "r"(v[21]), "r"(v[22]), "r"(v[23]),
+        "r"(v[24]), "r"(v[25]), "r"(v[26]),
+        "r"(v[27]), "r"(v[28]), "r"(v[29]),
+        "r"(v[30]), "r"(v[31])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16]) {
@@ -121,6 +112,56 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16]) 
       ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
+}
+
+// 32 columns without the wait, and the wait that the registers depend on.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+// (a0, a1) * b + c, and (a0, a1) + (b0, b1), two fp32 lanes per instruction.
+__device__ __forceinline__ float2 fma2(float a0, float a1, float b, float c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mov.b64 z, {%5, %5};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float b0, float b1) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b0), "f"(b1));
+  return d;
 }
 
 __device__ __forceinline__ __half2 as_h2(uint32_t x) {
@@ -150,61 +191,100 @@ struct ChunkArgs {
   uint16_t* out;
   long long out_ts, out_hs;
   Work wk;
-  int lead, rt;     // rt: 256 (two row tiles) or 128 (one, even and odd tiles apart)
+  Grain grain;
+  uint8_t* plans;   // plan_bytes for each CTA: shared memory has no room
+  int rt;           // 256 (two row tiles) or 128 (one, even and odd tiles apart)
 };
 
+// Shared memory.  The pages pass through the ring in halves of a tile (4 blocks); the one-tile
+// form has one query tile less and a ring of six halves instead of three (there a key tile is
+// wanted two tiles ahead).
 template <int D>
 struct Smem {
-  static constexpr int kQ = 0;                              // 2 x [128 rows][D]
-  static constexpr int kQBytes = 128 * D * 2;
-  static constexpr int kK = kQ + 2 * kQBytes;               // 2 x [128 tokens][D]
-  static constexpr int kKBytes = kTile * D * 2;
-  static constexpr int kV = kK + 2 * kKBytes;               // [D channels][128 tokens]
-  static constexpr int kVBytes = D * kTile * 2;
-  static constexpr int kRing = kV + kVBytes;                // 2 x 8 blocks
-  static constexpr int kRingBytes = 8 * 20 * D;
-  static constexpr int kMl = kRing + 2 * kRingBytes;        // [128][2]: stream 1's m, l
+  static constexpr int kTileBytes = 128 * D * 2;            // any operand tile
+  static constexpr int kK = 0;                              // 2 x [128 tokens][D]
+  static constexpr int kV = kK + 2 * kTileBytes;            // 2 x [D channels][128 tokens]
+  static constexpr int kQ = kV + 2 * kTileBytes;            // [128 rows][D], two in the two-tile form
+  static constexpr int kHalfBytes = 4 * 20 * D;             // 4 blocks
+  static constexpr int kMl = 0;                             // after the ring: [128][2], stream 1's m, l
   static constexpr int kBars = kMl + 128 * 8;
-  static constexpr int kPlan = kBars + 256;
+  static constexpr int kJobs = kBars + 320;                 // two pieces of work
+  static constexpr int kSlots = kJobs + 96;                 // the partition's place in its work
+  static constexpr int kEnd = kSlots + 64;
+  __host__ __device__ static constexpr int ring(bool dual) { return kQ + (dual ? 2 : 1) * kTileBytes; }
+  __host__ __device__ static constexpr int stages(bool dual) { return dual ? 3 : 6; }
+  __host__ __device__ static constexpr int rest(bool dual) { return ring(dual) + stages(dual) * kHalfBytes; }
+};
+
+// Position in the ring: stage and the phase of its barriers.
+struct RingPos {
+  uint32_t stage = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t stages) {
+    if (++stage == stages) {
+      stage = 0;
+      ++phase;
+    }
+  }
+};
+
+// A piece of work as the roles take it; two are on the way at once.
+struct Job {
+  int b, h, start;          // sequence, KV head, the sequence's first row
+  int row_first, rows;      // of the unit
+  int base_seen;            // tokens that the sequence's row 0 sees
+  int most;                 // tokens that the last row sees
+  int lo, n;                // first tile, tiles; n < 0: no more work
+  int slot;                 // of the partial, -1 if the unit is this piece
 };
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_kernel(const __grid_constant__ ChunkArgs a) {
   using S = Smem<D>;
-  constexpr int NG = D / 32, BB = 20 * D, kStride = D + 4;
+  constexpr int NG = D / 32, BB = 20 * D;
   extern __shared__ __align__(1024) uint8_t smem[];
   const Geo& g = a.g;
   const Batch& bt = a.bt;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
-  uint64_t* ring_full = bars;        // [2] the staged blocks are in
-  uint64_t* ring_empty = bars + 2;   // [2] both builders are done with them (8 warps)
-  uint64_t* k_full = bars + 4;       // [2] key tile written (4 warps)
-  uint64_t* k_empty = bars + 6;      // [2] its products are done
-  uint64_t* v_full = bars + 8;       // value tile written (4 warps)
-  uint64_t* v_empty = bars + 9;
-  uint64_t* s_full = bars + 10;      // [2] logits of the stream are in TMEM
-  uint64_t* p_full = bars + 12;      // [2] its weights are (4 warps)
-  uint64_t* o_done = bars + 14;      // [2] its value products of this piece are done
-  uint64_t* q_full = bars + 16;      // query tiles written (8 warps)
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 17);
-  volatile int* fail = reinterpret_cast<volatile int*>(bars + 18);
-  long long* cost = reinterpret_cast<long long*>(smem + S::kPlan);
-  int* units = reinterpret_cast<int*>(cost + bt.B + 1);
+  const bool dual = a.rt == 256;
+  uint8_t* rest = smem + S::rest(dual);
+  uint8_t* const ring0 = smem + S::ring(dual);
+  const uint32_t stages = S::stages(dual);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(rest + S::kBars);
+  uint64_t* ring_full = bars + 26;   // [6] the staged blocks are in
+  uint64_t* ring_empty = bars + 32;  // [6] both builders are done with them (8 warps)
+  uint64_t* k_full = bars;           // [2] key tile written (4 warps, two halves)
+  uint64_t* k_empty = bars + 2;      // [2] its products are done
+  uint64_t* v_full = bars + 4;       // [2] value tile written
+  uint64_t* v_empty = bars + 6;      // [2]
+  uint64_t* s_full = bars + 12;      // [2] logits of the stream are in TMEM
+  uint64_t* p_full = bars + 14;      // [2] its weights are (4 warps)
+  uint64_t* o_done = bars + 16;      // [2] its value products of this piece are done
+  uint64_t* q_full = bars + 18;      // query tiles written (8 warps)
+  uint64_t* job_full = bars + 19;    // [2]
+  uint64_t* job_empty = bars + 21;   // [2] every role is done with it (16 warps and two more)
+  uint64_t* drained = bars + 23;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 24);
+  volatile int* fail = reinterpret_cast<volatile int*>(bars + 25);
+  Job* jobs = reinterpret_cast<Job*>(rest + S::kJobs);
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 6; ++i) {
       mbar_init(ring_full + i, 1);
       mbar_init(ring_empty + i, 8);
-      mbar_init(k_full + i, 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, 8);
       mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, 8);
+      mbar_init(v_empty + i, 1);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
       mbar_init(o_done + i, 1);
+      mbar_init(job_full + i, 1);
+      mbar_init(job_empty + i, 18);
     }
-    mbar_init(v_full, 4);
-    mbar_init(v_empty, 1);
     mbar_init(q_full, 8);
+    mbar_init(drained, 1);
     *fail = 0;
     fence_mbar_init();
   }
@@ -216,10 +296,11 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
   }
   asm volatile("griddepcontrol.launch_dependents;");
   tc_fence_before();
-  build_plan<kThreads>(g, bt, a.rt, a.lead, cost, units, reinterpret_cast<long long*>(smem + S::kMl));
+  const Plan& plan =
+      build_plan<kThreads>(g, bt, a.rt, a.grain, a.plans + blockIdx.x * plan_bytes(bt.B),
+                           reinterpret_cast<long long*>(rest + S::kMl));
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const bool dual = a.rt == 256;
 
   // Bounded wait for phase `n` (counted from 0) of a barrier; false once anything in the CTA
   // gave up.
@@ -235,20 +316,14 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
     }
     return true;
   };
-  struct Span {
-    int lo, n;              // first tile, tiles
-    int rows, base_seen, row_first, most;
-  };
-  auto span_of = [&](const Piece& pc) {
-    Span s;
-    s.row_first = pc.tile * a.rt;
-    s.rows = min(a.rt, pc.T * g.G - s.row_first);
-    s.base_seen = pc.len - pc.T + 1;
-    s.most = max(0, s.base_seen + (s.row_first + s.rows - 1) / g.G);   // tokens the last row sees
-    const int nt = (s.most + kTile - 1) / kTile;
-    s.lo = min((pc.lo + kTile - 1) / kTile, nt);                        // the tiles that start in [lo, hi)
-    s.n = min((pc.hi + kTile - 1) / kTile, nt) - s.lo;
-    return s;
+  // The builders, the products and the staging take job after job this way.
+  auto for_each_job = [&](auto&& fn, bool arrives) {
+    for (uint32_t i = 0;; ++i) {
+      if (!wait(job_full + (i & 1u), i >> 1, kCommitLimit)) return;
+      const Job& jb = jobs[i & 1u];
+      if (jb.n < 0 || !fn(jb)) return;
+      if (arrives) mbar_arrive(job_empty + (i & 1u));
+    }
   };
 
   if (warp < 8) {
@@ -256,111 +331,180 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
     const int stream = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + 128 * stream, t_o = tmem + lanes + kTmemO + 128 * stream;
-    float* ml = reinterpret_cast<float*>(smem + S::kMl) + 2 * row;
+    float* ml = reinterpret_cast<float*>(rest + S::kMl) + 2 * row;
+    uint8_t* qa = smem + S::kQ + (dual ? stream * S::kTileBytes : 0);
     uint32_t ns = 0, no = 0;   // logit tiles taken; pieces whose value products were waited for
-    for_each_piece(g, bt, a.rt, a.lead, cost, units, a.wk, gridDim.x, tid == 0, [&](const Piece& pc) -> bool {
-      const Span sp = span_of(pc);
-      const int v = dual ? 128 * stream + row : row;     // row of the unit
-      const bool live = v < sp.rows;
-      const int r = sp.row_first + v, j = r / g.G, hg = r - j * g.G;
-      // ---- this thread's query row -> A (in the one-tile form stream 1 has stream 0's)
+    // whether any thread of the two streams says so (they go on or stop alike)
+    auto either = [&](bool x) -> bool {
+      uint32_t any;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+          : "=r"(any)
+          : "r"(static_cast<uint32_t>(x))
+          : "memory");
+      return any != 0;
+    };
+    bool ok = true;
+    for (uint32_t job = 0;; ++job) {
+      ok = ok && wait(job_full + (job & 1u), job >> 1, kCommitLimit);
+      // every thread is done with the last piece (its query tile, its O, ml)
+      if (either(!ok || *fail)) break;
+      const Job& jb = jobs[job & 1u];
+      const int nt = jb.n;
+      if (nt < 0) break;
+      const int v = (dual ? 128 * stream : 0) + row;     // row of the unit
+      const bool live = v < jb.rows;
+      // this thread's row: its token and head in a [tokens][heads][D] tensor
+      const int r = jb.row_first + v, j = r / g.G;
+      const int tok = live ? jb.start + j : -1, head = jb.h * g.G + r - j * g.G;
+      const int seen = live ? jb.base_seen + j : 0;
       float fac = 0.f;
-      {
-        uint8_t* qa = smem + S::kQ + stream * S::kQBytes;
-        const uint16_t* src = a.q.p + static_cast<long long>(pc.start + j) * a.q.ts + (pc.h * g.G + hg) * a.q.hs;
-        float top = 0.f;
-        for (int c = 0; live && c < D / 8; ++c) {
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + c);
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+      if (dual || stream == 0) {
+        // ---- the query rows -> A.  A warp takes its 32 rows eight at a time, four 16-byte pieces of
+        // each per instruction, so eight lanes' stores fill neighbouring 16-byte places.  The rows
+        // are copied as they are and scaled in place.
+        const int sub = lane & 7, part = lane >> 3;
+#pragma unroll 1
+        for (int ra = 0; ra < 4; ++ra) {
+          const int rtok = __shfl_sync(0xffffffffu, tok, 8 * ra + sub), rhead = __shfl_sync(0xffffffffu, head, 8 * ra + sub);
+          const uint16_t* src = a.q.p + rtok * a.q.ts + rhead * a.q.hs + 8 * part;
+          uint8_t* dst = qa + tile_off(128, 32 * (warp & 3) + 8 * ra + sub, 8 * part);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
-        }
-        const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-        const int up = top > 0.f ? min(max(-ex, -90), 120) : 0;      // largest channel to [1, 2)
-        const float mul = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-        fac = g.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (live) w = __ldg(reinterpret_cast<const uint4*>(src) + c);
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-          float f[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(x[i] << 16) * mul;
-            f[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u) * mul;
+          for (int c = 0; c < NG; ++c) {
+            if (rtok >= 0)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst + c * (2 * 128 * 32))),
+                           "l"(src + 32 * c)
+                           : "memory");
+            else
+              *reinterpret_cast<uint4*>(dst + c * (2 * 128 * 32)) = make_uint4(0u, 0u, 0u, 0u);
           }
-          // position order inside 8 channels: 0, 4, 1, 5, 2, 6, 3, 7, as a code word unpacks
-          *reinterpret_cast<uint4*>(qa + tile_off(128, row, 8 * c)) =
-              make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+        for (int ra = 0; ra < 4; ++ra) {
+          uint8_t* at = qa + tile_off(128, 32 * (warp & 3) + 8 * ra + sub, 8 * part);
+          uint32_t w[NG][4];
+          float top = 0.f;
+#pragma unroll
+          for (int c = 0; c < NG; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(at + c * (2 * 128 * 32));
+            w[c][0] = x.x; w[c][1] = x.y; w[c][2] = x.z; w[c][3] = x.w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[c][i] << 16)), fabsf(__uint_as_float(w[c][i] & 0xFFFF0000u))));
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+          const int up = top > 0.f ? min(max(-ex, -90), 120) : 0;      // largest channel to [1, 2)
+          const float mul = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+#pragma unroll
+          for (int c = 0; c < NG; ++c) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              f[2 * i] = __uint_as_float(w[c][i] << 16) * mul;
+              f[2 * i + 1] = __uint_as_float(w[c][i] & 0xFFFF0000u) * mul;
+            }
+            // position order inside 8 channels: 0, 4, 1, 5, 2, 6, 3, 7, as a code word unpacks
+            *reinterpret_cast<uint4*>(at + c * (2 * 128 * 32)) = make_uint4(
+                pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
+          }
+          // the row's owner takes its factor
+          const float mine = g.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+          const float got = __shfl_sync(0xffffffffu, mine, lane & 7);
+          if (part == ra) fac = got;
+        }
+        if (!dual) ml[0] = fac;
       }
       proxy_fence();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
-      const int seen = live ? sp.base_seen + j : 0;
+      if (!dual) {          // stream 1 has the same rows
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (stream == 1) fac = ml[0];
+      }
 
-      float ref = -1e30f, den = 0.f;
-      int mine = 0;       // tiles of this stream so far
-      bool ok = true;
-      for (int i = dual ? 0 : stream; i < sp.n; i += dual ? 1 : 2) {
+      float ref = -1e30f, den = 0.f;    // lower than any logit: the first one moves it
+      int mine = 0;                     // tiles of this stream so far
+      int lim = seen - (jb.lo + (dual ? 0 : stream)) * kTile;     // columns of the tile below it are visible
+      for (int i = dual ? 0 : stream; i < nt; i += dual ? 1 : 2, lim -= dual ? kTile : 2 * kTile) {
         if (!(ok = wait(s_full + stream, ns, kCommitLimit))) break;
         ++ns;
         tc_fence_after();
-        const int lim = seen - (sp.lo + i) * kTile;     // columns below it are visible
         const bool edge = __any_sync(0xffffffffu, lim < kTile);
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float x[32];
-          tmem_ld32(t_s + 32 * c, x);
+        // Weights of 32 columns from their logits (bits in, fp16 pairs out); their sum.
+        auto weights = [&](int col, uint32_t (&x)[32], uint32_t* p) {
           if (edge) {
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if (32 * c + k >= lim) x[k] = -INFINITY;
+              if (col + k >= lim) x[k] = 0xFF800000u;     // -inf
           }
+          const float off = -ref;
+          float2 d0 = make_float2(0.f, 0.f), d1 = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, x[k]);
-        }
-        mx *= fac;          // -inf (or NaN from 0 * inf in a row that is not live) if nothing is visible
-        bool move = mx > ref + kSlack;
-        if (__any_sync(0xffffffffu, move)) {
-          float f = 1.f;
-          if (move) {
-            f = ex2(ref - mx);
-            ref = mx;
-            den *= f;
+          for (int k = 0; k < 32; k += 4) {
+            const float2 e0 = fma2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]), fac, off);
+            const float2 e1 = fma2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]), fac, off);
+            const float p0 = ex2(e0.x), p1 = ex2(e0.y), p2 = ex2(e1.x), p3 = ex2(e1.y);
+            d0 = add2(d0, p0, p1);
+            d1 = add2(d1, p2, p3);
+            p[k / 2] = pack_f16x2(p0, p1);
+            p[k / 2 + 1] = pack_f16x2(p2, p3);
           }
-          if (mine > 0) {   // the commit of these logits covers the stream's earlier value products
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              tmem_ld32(t_o + 32 * c, o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= f;
-              tmem_st32(t_o + 32 * c, o);
-            }
-          }
-        }
-        const float off = -ref;
+          d0 = add2(d0, d1.x, d1.y);
+          return d0.x + d0.y;
+        };
+        // The weights of 32 columns stay in registers until their sum is found to be in range, so
+        // their logits can still be read again.
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          float x[32];
-          tmem_ld32(t_s + 32 * c, x);
-          uint32_t p[16];
-          float d0 = 0.f, d1 = 0.f;
+          uint32_t cur[32], p[16];
+          tmem_ld32_start(t_s + 32 * c, cur);
+          tmem_ld_wait(cur);
+          float sum = weights(32 * c, cur, p);
+          while (__any_sync(0xffffffffu, sum > kTop)) {
+            // the reference of some row moves up (the commit of these logits covers the stream's
+            // earlier value products, so O is idle)
+            uint32_t y[16];
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int k = 32 * c; k < 32 * c + 32; k += 16) {
+              tmem_ld16(t_s + k, y);
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float p0 = ex2(fmaf(x[k], fac, off)), p1 = ex2(fmaf(x[k + 1], fac, off));
-            if (edge) {
-              if (32 * c + k >= lim) p0 = 0.f;
-              if (32 * c + k + 1 >= lim) p1 = 0.f;
+              for (int e = 0; e < 16; ++e)
+                if (k + e < lim) mx = fmaxf(mx, __uint_as_float(y[e]));
             }
-            d0 += p0;
-            d1 += p1;
-            p[k / 2] = pack_f16x2(p0, p1);
+            float f = 1.f;
+            if (sum > kTop) {      // some weight is 2^10 at least
+              const float to = ceilf(mx * fac);
+              f = ex2(ref - to);
+              ref = to;
+              den *= f;
+            }
+            if (mine > 0) {
+#pragma unroll 1
+              for (int k = 0; k < D; k += 16) {
+                tmem_ld16(t_o + k, y);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+                tmem_st16(t_o + k, y);
+              }
+            }
+            tmem_wait_st();
+            const __half2 f2 = __float2half2_rn(f);
+#pragma unroll 1
+            for (int k = 0; k < 16 * c; k += 16) {     // this tile's weights that are written already
+              tmem_ld16(t_s + k, y);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = as_u32(__hmul2(as_h2(y[e]), f2));
+              tmem_st16(t_s + k, y);
+            }
+            tmem_ld32_start(t_s + 32 * c, cur);
+            tmem_ld_wait(cur);
+            sum = weights(32 * c, cur, p);
           }
-          den += d0 + d1;
+          den += sum;
           tmem_st16(t_s + 16 * c, p);     // over columns that were read
         }
         tmem_wait_st();
@@ -391,84 +535,98 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
         }
       }
       if (dual || stream == 0) {
-        const bool has0 = mine > 0, has1 = !dual && sp.n > 1;
+        const int slot = jb.slot;
+        const bool has0 = mine > 0, has1 = !dual && nt > 1;
         const float inv = den == 0.f ? 0.f : 1.f / den;
-        float* part = a.wk.part + (static_cast<size_t>(pc.slot) * a.rt + v) * kStride;
-        uint16_t* dst = a.out + static_cast<long long>(pc.start + j) * a.out_ts + (pc.h * g.G + hg) * a.out_hs;
-        if (!pc.whole && live) *reinterpret_cast<float2*>(part) = make_float2(ref, den);
+        float* part = part_of<D>(a.wk.part, slot, a.rt);
+        if (slot >= 0 && live) reinterpret_cast<float2*>(part)[v] = make_float2(ref, den);
+        // the stream's logits are done, so its query tile is free to turn the rows around in
+        uint8_t* turn = qa + (warp & 3) * (64 * D);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
+        for (int c = 0; c < NG; ++c) {
+          uint32_t o[32];
           if (has0) {
-            tmem_ld32(t_o + 32 * c, o);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0.f;
+            tmem_ld32_start(t_o + 32 * c, o);
+            tmem_ld_wait(o);
           }
-          if (w0 != 1.f) {
+          if (!has0 || w0 != 1.f) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = w0 == 0.f ? 0.f : o[k] * w0;
+            for (int k = 0; k < 32; ++k)
+              o[k] = !has0 || w0 == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * w0);
           }
           if (has1) {
-            float o1[32];
-            tmem_ld32(t_o + 128 + 32 * c, o1);
+            uint32_t o1[32];
+            tmem_ld32_start(t_o + 128 + 32 * c, o1);
+            tmem_ld_wait(o1);
             if (w1 != 0.f) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = fmaf(o1[k], w1, o[k]);
+              for (int k = 0; k < 32; ++k)
+                o[k] = __float_as_uint(fmaf(__uint_as_float(o1[k]), w1, __uint_as_float(o[k])));
             }
           }
           // column 8 i + w of a group is channel 4 w + i
-          if (live && pc.whole) {
+          if (slot < 0) {
 #pragma unroll
             for (int h = 0; h < 4; ++h) {      // channels 8 h .. 8 h + 7: w = 2 h, 2 h + 1
               uint32_t wd[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const int w = 2 * h + (k >> 1), i = 2 * (k & 1);
-                const float x0 = den == 0.f ? 0.f : o[8 * i + w] * inv, x1 = den == 0.f ? 0.f : o[8 * (i + 1) + w] * inv;
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(x0, x1);
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * i + w]) * inv,
+                                                                __uint_as_float(o[8 * (i + 1) + w]) * inv);
                 memcpy(&wd[k], &b2, 4);
               }
-              *reinterpret_cast<uint4*>(dst + 32 * c + 8 * h) = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+              *reinterpret_cast<uint4*>(turn + lane * (2 * D) + (((4 * c + h) ^ (lane & 7)) * 16)) =
+                  make_uint4(wd[0], wd[1], wd[2], wd[3]);
             }
           } else if (live) {
 #pragma unroll
             for (int w = 0; w < 8; ++w)
-              *reinterpret_cast<float4*>(part + 4 + 32 * c + 4 * w) = make_float4(o[w], o[8 + w], o[16 + w], o[24 + w]);
+              reinterpret_cast<uint4*>(part + 2 * a.rt)[(8 * c + w) * a.rt + v] =
+                  make_uint4(o[w], o[8 + w], o[16 + w], o[24 + w]);
+          }
+        }
+        if (slot < 0) {
+          __syncwarp();
+          constexpr int kPer = 32 / (D / 8);     // rows a warp writes at once
+          const int piece = lane & (D / 8 - 1);
+#pragma unroll 1
+          for (int x = lane / (D / 8); x < 32; x += kPer) {
+            const int rtok = __shfl_sync(0xffffffffu, tok, x), rhead = __shfl_sync(0xffffffffu, head, x);
+            const uint4 w = *reinterpret_cast<const uint4*>(turn + x * (2 * D) + ((piece ^ (x & 7)) * 16));
+            if (rtok >= 0)
+              *(reinterpret_cast<uint4*>(a.out + rtok * a.out_ts + rhead * a.out_hs) + piece) = w;
           }
         }
       }
       tc_fence_before();
-      // both streams are done with TMEM, and go on or stop alike
-      uint32_t stop;
-      asm volatile(
-          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
-          : "=r"(stop)
-          : "r"(static_cast<uint32_t>(!ok || *fail))
-          : "memory");
-      return !stop;
-    });
+      __syncwarp();
+      if (lane == 0) mbar_arrive(job_empty + (job & 1u));
+    }
   } else if (warp < 12) {
     // ================================================================ key tiles
-    const int t = tid - 256;                   // token of the tile
+    const int t = tid & 63, pieces = ((tid >> 6) & 1) * 2;      // token of the half, two of its row's pieces
     const int blk = t >> 4, r = t & 15;
-    uint32_t nr = 0;                            // tiles so far
-    for_each_piece(g, bt, a.rt, a.lead, cost, units, a.wk, gridDim.x, false, [&](const Piece& pc) -> bool {
-      const Span sp = span_of(pc);
-      for (int i = 0; i < sp.n; ++i, ++nr) {
-        const uint32_t buf = nr & 1u;
-        if (!wait(ring_full + buf, nr >> 1, g.wait_limit)) return false;
-        if (nr >= 2 && !wait(k_empty + buf, (nr >> 1) - 1, kCommitLimit)) return false;
-        const uint8_t* src = smem + S::kRing + buf * S::kRingBytes + blk * BB;
-        uint8_t* dst = smem + S::kK + buf * S::kKBytes;
-        const bool there = (sp.lo + i) * kTile + t < sp.most;    // behind: whatever the page holds
+    uint32_t nr = 0;                            // halves so far
+    RingPos rp;
+    for_each_job([&](const Job& jb) -> bool {
+      const int n = 2 * jb.n;
+      int left = jb.most - jb.lo * kTile;       // tokens from the half's first on
+      __syncwarp();
+      for (int i = 0; i < n; ++i, ++nr, left -= kTile / 2) {
+        const uint32_t buf = (nr >> 1) & 1u;
+        if (!wait(ring_full + rp.stage, rp.phase, g.wait_limit)) return false;
+        if (nr >= 4 && !(nr & 1u) && !wait(k_empty + buf, (nr >> 2) - 1, kCommitLimit)) return false;
+        const uint8_t* src = ring0 + rp.stage * S::kHalfBytes + blk * BB;
+        uint8_t* dst = smem + S::kK + buf * S::kTileBytes + tile_off(kTile, 64 * (nr & 1u) + t, 0);
+        const bool there = t < left;            // behind: whatever the page holds
         uint32_t sz[NG];
 #pragma unroll
         for (int k = 0; k < NG; ++k)
           sz[k] = there ? *reinterpret_cast<const uint32_t*>(src + 8 * D + r * (4 * NG) + 4 * k) : 0u;
 #pragma unroll
-        for (int pp = 0; pp < 4; ++pp) {
-          const int piece = pp ^ ((t >> 1) & 3);     // eight lanes' pieces lie in different banks
+        for (int pp = 0; pp < 2; ++pp) {
+          const int piece = (pieces + pp) ^ ((t >> 1) & 3);     // eight lanes' pieces lie in different banks
           uint32_t w[NG];
           const uint8_t* at = src + r * (D / 2) + piece * (4 * NG);
           if constexpr (NG == 4) {
@@ -484,7 +642,7 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
             const uint32_t w8 = w[k] >> 8;
             const uint32_t x0 = as_u32(__hfma2(codes_low(w[k]), s, z)), x1 = as_u32(__hfma2(codes_high(w[k]), s, z));
             const uint32_t x2 = as_u32(__hfma2(codes_low(w8), s, z)), x3 = as_u32(__hfma2(codes_high(w8), s, z));
-            *reinterpret_cast<uint4*>(dst + tile_off(kTile, t, 32 * k) + (piece >> 1) * (kTile * 32) + (piece & 1) * 128) =
+            *reinterpret_cast<uint4*>(dst + (2 * k + (piece >> 1)) * (kTile * 32) + (piece & 1) * 128) =
                 make_uint4(x0, x1, x2, x3);
           }
         }
@@ -492,47 +650,40 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(k_full + buf);
-          mbar_arrive(ring_empty + buf);
+          mbar_arrive(ring_empty + rp.stage);
         }
+        rp.next(stages);
       }
       return true;
-    });
+    }, lane == 0);
   } else if (warp < 16) {
     // ================================================================ value tiles
     const int bw = warp - 12;
     const int w = lane & 7, half = (lane >> 3) & 1, odd = lane >> 4;   // piece, pair of groups, octet parity
     uint32_t nr = 0;
-    for_each_piece(g, bt, a.rt, a.lead, cost, units, a.wk, gridDim.x, false, [&](const Piece& pc) -> bool {
-      const Span sp = span_of(pc);
-      for (int i = 0; i < sp.n; ++i, ++nr) {
-        const uint32_t buf = nr & 1u;
-        if (!wait(ring_full + buf, nr >> 1, g.wait_limit)) return false;
-        if (nr >= 1 && !wait(v_empty, nr - 1, kCommitLimit)) return false;
-        const uint8_t* ring = smem + S::kRing + buf * S::kRingBytes + 10 * D;
-        uint8_t* dst = smem + S::kV;
-        const int left = sp.most - (sp.lo + i) * kTile;
-        constexpr int kHalves = NG / 2;                   // pairs of channel groups
-#pragma unroll
-        for (int rep = 0; rep < 2; ++rep) {
-          // an item: 8 tokens (octet), piece w, one pair of groups; D = 64 has one pair, so the
-          // `half` bit names two more octets
-          int octet, pair;
-          if constexpr (kHalves == 2) {
-            octet = 4 * bw + 2 * rep + odd;
-            pair = half;
-          } else {
-            octet = 4 * bw + 2 * half + odd;
-            pair = 0;
-          }
-          if (kHalves == 1 && rep) break;
-          const uint8_t* blk = ring + (octet >> 1) * BB;
-          const int r0 = (octet & 1) * 8;
+    RingPos rp;
+    for_each_job([&](const Job& jb) -> bool {
+      const int n = 2 * jb.n;
+      int left = jb.most - jb.lo * kTile;
+      __syncwarp();
+      for (int i = 0; i < n; ++i, ++nr, left -= kTile / 2) {
+        const uint32_t buf = (nr >> 1) & 1u;
+        if (!wait(ring_full + rp.stage, rp.phase, g.wait_limit)) return false;
+        if (nr >= 4 && !(nr & 1u) && !wait(v_empty + buf, (nr >> 2) - 1, kCommitLimit)) return false;
+        // an item: 8 tokens (octet of the half), piece w, one pair of groups.  With D = 64 there is
+        // one pair: half of the lanes have nothing to do.
+        constexpr bool kAll = NG == 4;
+        const int octet = 2 * bw + odd, pair = kAll ? half : 0;
+        if (kAll || half == 0) {
+          const uint8_t* blk = ring0 + rp.stage * S::kHalfBytes + 10 * D + (octet >> 1) * BB;
+          uint8_t* dst = smem + S::kV + buf * S::kTileBytes + (4 * (nr & 1u) + (octet >> 1)) * (D * 32) +
+                         (octet & 1) * 128 + w * 16;
           uint32_t cw[8], sz[8][2];
           // lanes of odd octets take each token pair the other way round: the two octets of a warp
           // then read rows of different parity
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int t = r0 + (k ^ odd);
+            const int t = (octet & 1) * 8 + (k ^ odd);
             cw[k] = *reinterpret_cast<const uint32_t*>(blk + t * (D / 2) + value_place<D>(t, w) * (2 * NG) + 4 * pair);
             const uint2 x = *reinterpret_cast<const uint2*>(blk + 8 * D + t * (4 * NG) + 8 * pair);
             const bool there = 8 * octet + (k ^ odd) < left;
@@ -556,43 +707,43 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
             }
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch)        // value row (4 group + ch) * 8 + w
-              *reinterpret_cast<uint4*>(dst + (octet >> 1) * (D * 32) + (octet & 1) * 128 +
-                                        (4 * (2 * pair + gp) + ch) * 256 + w * 16) =
+              *reinterpret_cast<uint4*>(dst + (4 * (2 * pair + gp) + ch) * 256) =
                   make_uint4(x[ch][0], x[ch][1], x[ch][2], x[ch][3]);
           }
         }
         proxy_fence();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(v_full);
-          mbar_arrive(ring_empty + buf);
+          mbar_arrive(v_full + buf);
+          mbar_arrive(ring_empty + rp.stage);
         }
+        rp.next(stages);
       }
       return true;
-    });
-  } else if (warp == 16) {
-    // ================================================================ products
-    if (lane == 0) {
+    }, lane == 0);
+  } else {
+    if (warp == 16 && lane == 0) {
+      // ============================================================== products
       const uint32_t q0 = smem_u32(smem + S::kQ), k0 = smem_u32(smem + S::kK), v0 = smem_u32(smem + S::kV);
       constexpr uint32_t kIdescS = mma_idesc(kTile), kIdescO = mma_idesc(D);
-      uint32_t nk = 0, nv = 0, nq = 0, np[2] = {0, 0};   // tiles taken, query tiles, weights taken
+      uint32_t nk = 0, nv = 0, nq = 0, np0 = 0, np1 = 0;   // tiles, query tiles, weights of either stream taken
       auto logits = [&](int stream, uint32_t buf) {
-        const uint64_t qa = tile_desc(q0 + stream * S::kQBytes), kb = tile_desc(k0 + buf * S::kKBytes);
+        const uint64_t qd = tile_desc(q0 + (dual ? stream * S::kTileBytes : 0)), kd = tile_desc(k0 + buf * S::kTileBytes);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
-          mma_ss(tmem + 128 * stream, qa + s * (128 * 32 >> 4), kb + s * (kTile * 32 >> 4), kIdescS, s > 0);
+          mma_ss(tmem + 128 * stream, qd + s * (128 * 32 >> 4), kd + s * (kTile * 32 >> 4), kIdescS, s > 0);
         tc_commit(s_full + stream);
       };
-      auto values = [&](int stream, bool accumulate, bool last) {
-        const uint64_t vb = tile_desc(v0);
+      auto values = [&](int stream, uint32_t buf, bool accumulate, bool last) {
+        const uint64_t vd = tile_desc(v0 + buf * S::kTileBytes);
 #pragma unroll
         for (int s = 0; s < kTile / 16; ++s)
-          mma_ts(tmem + kTmemO + 128 * stream, tmem + 128 * stream + 8 * s, vb + s * (D * 32 >> 4), kIdescO,
+          mma_ts(tmem + kTmemO + 128 * stream, tmem + 128 * stream + 8 * s, vd + s * (D * 32 >> 4), kIdescO,
                  accumulate || s > 0);
         if (last) tc_commit(o_done + stream);
       };
-      for_each_piece(g, bt, a.rt, a.lead, cost, units, a.wk, gridDim.x, false, [&](const Piece& pc) -> bool {
-        const Span sp = span_of(pc);
+      for_each_job([&](const Job& jb) -> bool {
+        const int n = jb.n, ahead = dual ? 1 : 2;
         if (!wait(q_full, nq++, kCommitLimit)) return false;
         tc_fence_after();
         // the next key tile, once written
@@ -601,23 +752,24 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
           tc_fence_after();
           return true;
         };
-        const int ahead = dual ? 1 : 2;
-        for (int i = 0; i < ahead && i < sp.n; ++i) {
+        for (int i = 0; i < ahead && i < n; ++i) {
           if (!key_tile()) return false;
           logits(dual ? 0 : i, nk & 1u);
           if (dual) logits(1, nk & 1u);
           tc_commit(k_empty + (nk & 1u));
           ++nk;
         }
-        for (int i = 0; i < sp.n; ++i) {
+        for (int i = 0; i < n; ++i) {
           for (int x = 0; x < (dual ? 2 : 1); ++x) {
             const int stream = dual ? x : i & 1;
-            if (!wait(p_full + stream, np[stream]++, kCommitLimit)) return false;
-            if (x == 0 && !wait(v_full, nv++, kCommitLimit)) return false;
+            if (x == 0 && !wait(v_full + (nv & 1u), nv >> 1, kCommitLimit)) return false;
+            if (!wait(p_full + stream, stream ? np1 : np0, kCommitLimit)) return false;
+            if (stream) ++np1;
+            else ++np0;
             tc_fence_after();
-            values(stream, i >= ahead, i + ahead >= sp.n);
-            if (x == (dual ? 1 : 0)) tc_commit(v_empty);
-            if (i + ahead < sp.n) {
+            values(stream, nv & 1u, i >= ahead, i + ahead >= n);
+            if (x == (dual ? 1 : 0)) tc_commit(v_empty + (nv++ & 1u));
+            if (i + ahead < n) {
               if (x == 0 && !key_tile()) return false;
               logits(stream, nk & 1u);
               if (x == (dual ? 1 : 0)) {
@@ -628,67 +780,99 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
           }
         }
         return true;
+      }, true);
+    }
+    if (warp == 17) {
+      // ============================================================== staging
+      uint32_t nr = 0;
+      RingPos rp;
+      const size_t head_bytes = static_cast<size_t>(1 << (g.page_shift - 4)) * BB, page_bytes = head_bytes * g.Hkv;
+      const int per_copy = min(g.page_shift, 6);       // log2 tokens of a copy: 16 to 64 of a page
+      const int copies = (kTile / 2) >> per_copy;
+      for_each_job([&](const Job& jb) -> bool {
+        const int n = 2 * jb.n, first = jb.lo * kTile, most = jb.most;
+        const int32_t* table = bt.table + static_cast<size_t>(jb.b) * bt.max_pages;
+        const uint8_t* base = g.pages + static_cast<size_t>(jb.h) * head_bytes;
+        __syncwarp();
+        auto page_of = [&](int i) {        // of this lane's copy of half i
+          const int tok = first + i * (kTile / 2) + (lane << per_copy);
+          if (lane >= copies || i >= n || tok >= most) return 0;
+          const int id = __ldg(table + (tok >> g.page_shift));
+          if (id >= 0 && id < g.n_pages) return id;
+          raise(g.error, PNMIX_DEVERR_PAGE);
+          return 0;
+        };
+        int id = page_of(0);
+        for (int i = 0; i < n; ++i, ++nr) {
+          if (nr >= stages && !__all_sync(0xffffffffu, wait(ring_empty + rp.stage, rp.phase - 1, kCommitLimit))) return false;
+          const int tok = first + i * (kTile / 2) + (lane << per_copy);
+          // blocks of the half (the second half of a last tile may have none) and of this lane's copy
+          const int blocks = max(0, min(4, (most - first - i * (kTile / 2) + 15) >> 4));
+          const int mine = min(1 << (per_copy - 4), blocks - (lane << (per_copy - 4)));
+          if (lane == 0) {
+            proxy_fence();
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(ring_full + rp.stage)),
+                         "r"(blocks * BB)
+                         : "memory");
+          }
+          __syncwarp();
+          if (lane < copies && mine > 0)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             smem_u32(ring0 + rp.stage * S::kHalfBytes) + (lane << (per_copy - 4)) * BB),
+                         "l"(base + id * page_bytes + static_cast<size_t>((tok & ((1 << g.page_shift) - 1)) >> 4) * BB),
+                         "r"(mine * BB), "r"(smem_u32(ring_full + rp.stage))
+                         : "memory");
+          id = page_of(i + 1);
+          rp.next(stages);
+        }
+        return true;
+      }, lane == 0);
+      // every staged copy lands before the CTA's shared memory is given up
+      for (uint32_t k = 0; k < stages && k < nr; ++k) {
+        const uint32_t last = (nr - 1 - k) / stages;      // phase of the stage's last use
+        uint64_t* bar = ring_full + (nr - 1 - k) % stages;
+        for (uint32_t spins = 0; spins < g.wait_limit && !mbar_try_wait(bar, last & 1u); ++spins) {
+        }
+      }
+    }
+    if (warp == 18 && lane == 0) {
+      // ============================================================== the pieces of work
+      uint32_t i = 0;
+      auto give = [&](const Job& jb) -> bool {
+        if (i >= 2 && !wait(job_empty + (i & 1u), (i >> 1) - 1, kCommitLimit)) return false;
+        jobs[i & 1u] = jb;
+        mbar_arrive(job_full + (i & 1u));
+        ++i;
+        return true;
+      };
+      bool more = true;
+      for_each_piece<true>(g, bt, a.rt, plan, a.wk, reinterpret_cast<PieceSlot*>(rest + S::kSlots), true,
+                           [&](const Piece& pc) -> bool {
+        Job jb;
+        jb.b = pc.b;
+        jb.h = pc.h;
+        jb.start = pc.start;
+        jb.row_first = pc.tile * a.rt;
+        jb.rows = min(a.rt, pc.T * g.G - jb.row_first);
+        jb.base_seen = pc.len - pc.T + 1;
+        jb.most = max(0, jb.base_seen + (jb.row_first + jb.rows - 1) / g.G);
+        const int nt = (jb.most + kTile - 1) / kTile;
+        jb.lo = min((pc.lo + kTile - 1) / kTile, nt);                        // the tiles that start in [lo, hi)
+        jb.n = min((pc.hi + kTile - 1) / kTile, nt) - jb.lo;
+        jb.slot = pc.whole ? -1 : pc.slot;
+        return more = give(jb);
       });
+      Job end{};
+      end.n = -1;
+      if (more) give(end);
     }
     __syncwarp();
-  } else {
-    // ================================================================ staging
-    uint32_t nr = 0;
-    const size_t head_bytes = static_cast<size_t>(1 << (g.page_shift - 4)) * BB, page_bytes = head_bytes * g.Hkv;
-    const int per_copy = g.page_shift > 7 ? 7 : g.page_shift;       // log2 tokens of a copy
-    const int copies = kTile >> per_copy;
-    uint32_t landed = 0;
-    for_each_piece(g, bt, a.rt, a.lead, cost, units, a.wk, gridDim.x, false, [&](const Piece& pc) -> bool {
-      const Span sp = span_of(pc);
-      const int32_t* table = bt.table + static_cast<size_t>(pc.b) * bt.max_pages;
-      const uint8_t* base = g.pages + static_cast<size_t>(pc.h) * head_bytes;
-      auto page_of = [&](int i) {        // of this lane's copy of tile i
-        const int tok = (sp.lo + i) * kTile + (lane << per_copy);
-        if (lane >= copies || i >= sp.n || tok >= sp.most) return 0;
-        const int id = __ldg(table + (tok >> g.page_shift));
-        if (id >= 0 && id < g.n_pages) return id;
-        raise(g.error, PNMIX_DEVERR_PAGE);
-        return 0;
-      };
-      int id = page_of(0);
-      for (int i = 0; i < sp.n; ++i, ++nr) {
-        const uint32_t buf = nr & 1u;
-        if (nr >= 2 && !__all_sync(0xffffffffu, wait(ring_empty + buf, (nr >> 1) - 1, kCommitLimit))) return false;
-        const int tok = (sp.lo + i) * kTile + (lane << per_copy);
-        const int blocks = min(8, (sp.most - (sp.lo + i) * kTile + 15) >> 4);       // of the tile
-        const int mine = min(1 << (per_copy - 4), blocks - (lane << (per_copy - 4)));
-        if (lane == 0) {
-          proxy_fence();
-          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(ring_full + buf)),
-                       "r"(blocks * BB)
-                       : "memory");
-        }
-        __syncwarp();
-        if (lane < copies && mine > 0)
-          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                           smem_u32(smem + S::kRing + buf * S::kRingBytes) + (lane << (per_copy - 4)) * BB),
-                       "l"(base + id * page_bytes + static_cast<size_t>((tok & ((1 << g.page_shift) - 1)) >> 4) * BB),
-                       "r"(mine * BB), "r"(smem_u32(ring_full + buf))
-                       : "memory");
-        id = page_of(i + 1);
-      }
-      return true;
-    });
-    // every staged copy lands before the CTA's shared memory is given up
-    landed = nr >= 2 ? nr - 2 : 0;
-    for (; landed < nr; ++landed) {
-      uint32_t spins = 0;
-      while (!mbar_try_wait(ring_full + (landed & 1u), (landed >> 1) & 1u) && ++spins < g.wait_limit) {
-      }
-    }
   }
   __syncthreads();
   // After a stop products may still run: they are done before TMEM and the tiles are given up.
   if (*fail && warp == 16 && lane == 0) {
-    mbar_init(bars + 24, 1);
-    fence_mbar_init();
-    tc_commit(bars + 24);
-    for (uint32_t spins = 0; spins < kCommitLimit && !mbar_try_wait(bars + 24, 0u); ++spins) {
+    tc_commit(drained);
+    for (uint32_t spins = 0; spins < kCommitLimit && !mbar_try_wait(drained, 0u); ++spins) {
     }
   }
   tc_fence_before();
@@ -702,9 +886,9 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
 constexpr int kMaxDevices = 64;
 
 template <int D>
-static cudaError_t launch_chunk_d(ChunkArgs& a, cudaStream_t s) {
+static cudaError_t launch_chunk_d(const ChunkArgs& a, int* ctas, cudaStream_t s) {
   static std::atomic<int> cache[kMaxDevices];
-  const size_t smem = Smem<D>::kPlan + plan_bytes(a.bt.B);
+  const size_t smem = Smem<D>::rest(a.rt == 256) + Smem<D>::kEnd;
   auto kern = chunk_kernel<D>;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -713,17 +897,18 @@ static cudaError_t launch_chunk_d(ChunkArgs& a, cudaStream_t s) {
   if (known) sms = cache[dev].load(std::memory_order_relaxed);
   if (sms == 0) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(Smem<D>::kPlan + plan_bytes(kMaxBatch)))) != cudaSuccess ||
+                                  Smem<D>::rest(true) + Smem<D>::kEnd)) != cudaSuccess ||
         (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
       return e;
     if (known) cache[dev].store(sms, std::memory_order_relaxed);
   }
-  kern<<<sms < kMaxChunkCtas ? sms : kMaxChunkCtas, kThreads, smem, s>>>(a);
+  *ctas = sms < kMaxChunkCtas ? sms : kMaxChunkCtas;
+  kern<<<*ctas, kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_chunk(const Geo& g, const Batch& bt, const Rows& q, const pnmix_rows& out, const Work& wk, int rt,
-                         cudaStream_t s) {
+cudaError_t launch_chunk(const Geo& g, const Batch& bt, const Rows& q, const pnmix_rows& out, const Work& wk, uint8_t* plans,
+                         int rt, int* ctas, cudaStream_t s) {
   ChunkArgs a{};
   a.g = g;
   a.bt = bt;
@@ -732,9 +917,10 @@ cudaError_t launch_chunk(const Geo& g, const Batch& bt, const Rows& q, const pnm
   a.out_ts = out.token_stride;
   a.out_hs = out.head_stride;
   a.wk = wk;
-  a.lead = 256;
+  a.grain = {256, 256};
+  a.plans = plans;
   a.rt = rt;
-  return g.D == 64 ? launch_chunk_d<64>(a, s) : launch_chunk_d<128>(a, s);
+  return g.D == 64 ? launch_chunk_d<64>(a, ctas, s) : launch_chunk_d<128>(a, ctas, s);
 }
 
 }  // namespace kv4

@@ -78,7 +78,7 @@ struct AttnArgs {
   uint16_t* out;
   long long out_ts, out_hs;
   Work wk;
-  int lead;
+  Grain grain;
 };
 
 template <int D, int NT>
@@ -93,15 +93,14 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
   float* merge = reinterpret_cast<float*>(smem);           // [kWarps][RT][kStride], after the ring's use
   __shared__ uint64_t bars[kWarps][kStages];
   __shared__ long long tmp[2 * kWarps];
-  long long* cost = reinterpret_cast<long long*>(smem + kWarps * kStages * kStageBytes);
-  int* units = reinterpret_cast<int*>(cost + bt.B + 1);
+  __shared__ PieceSlot slots[kWarps];
   uint64_t* full = bars[warp];
   if (lane == 0) {
     for (int k = 0; k < kStages; ++k) mbar_init(full + k, 1);
     fence_mbar_init();
   }
   asm volatile("griddepcontrol.launch_dependents;");
-  build_plan<kThreads>(g, bt, RT, a.lead, cost, units, tmp);
+  const Plan& plan = build_plan<kThreads>(g, bt, RT, a.grain, smem + kWarps * kStages * kStageBytes, tmp);
 
   // tokens of this lane inside a block: A rows gq and gq + 8 (keys), tq's four (values)
   const int r0 = (gq & 1) ? 7 - (gq >> 1) : gq >> 1;
@@ -113,7 +112,7 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
   uint32_t nis = 0, ncons = 0;   // stages this warp issued and consumed
   bool dead = false;             // a staging wait ran out
 
-  for_each_piece(g, bt, RT, a.lead, cost, units, a.wk, gridDim.x, tid == 0, [&](const Piece& pc) -> bool {
+  for_each_piece<false>(g, bt, RT, plan, a.wk, slots + warp, tid == 0, [&](const Piece& pc) -> bool {
     const int row_first = pc.tile * RT, nrows = min(RT, pc.T * g.G - row_first);
     // tokens that row r sees, and the tile's most
     const int base_seen = pc.len - pc.T + 1;
@@ -483,9 +482,9 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
         *reinterpret_cast<uint2*>(a.out + static_cast<long long>(pc.start + j) * a.out_ts +
                                   (pc.h * g.G + hg) * a.out_hs + 4 * c4) = pk;
       } else {
-        float* part = a.wk.part + (static_cast<size_t>(pc.slot) * RT + v) * kStride;
-        if (c4 == 0) *reinterpret_cast<float2*>(part) = make_float2(m, l);
-        *reinterpret_cast<float4*>(part + 4 + 4 * c4) = o;
+        float* part = part_of<D>(a.wk.part, pc.slot, RT);
+        if (c4 == 0) reinterpret_cast<float2*>(part)[v] = make_float2(m, l);
+        reinterpret_cast<float4*>(part + 2 * RT)[c4 * RT + v] = o;
       }
     }
     __syncthreads();
@@ -493,58 +492,67 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
   });
 }
 
-// out_r = sum_s O_s 2^(m_s - m*) / sum_s l_s 2^(m_s - m*) over the partials of a unit's row;
-// one warp per row, D / 32 channels per lane.
+// out_r = sum_s O_s 2^(m_s - m*) / sum_s l_s 2^(m_s - m*) over the partials of a unit's rows.
+// CTA x takes the unit that begins in CTA x of the launch before, 8 rows of it (rows inner, as
+// the partials lie), and turns them around in shared memory
+// for the stores.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 merge_kernel(const __grid_constant__ AttnArgs a, int RT) {
-  constexpr int C = D / 32, kStride = D + 4;
+  constexpr int C4 = D / 4, kRows = 8, kLanes = kThreads / kRows;    // threads per row
+  __shared__ float2 out_tile[kRows][C4 + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int unit = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (unit >= *a.wk.count) return;
-  const UnitInfo f = a.wk.info[unit];
-  if (f.first < 0) return;
+  const int first = blockIdx.x;
+  const UnitInfo f = a.wk.info[first];
+  if (f.last < 0) return;
   int start, T;
   seq_rows(a.bt, f.b, start, T);
-  const int nrows = min(RT, T * a.g.G - f.tile * RT), n = f.last - f.first + 1;
-  const size_t slot_floats = static_cast<size_t>(RT) * kStride;
-  for (int v = blockIdx.y * kWarps + warp; v < nrows; v += kWarps * gridDim.y) {
-    const float* base = a.wk.part + static_cast<size_t>(v) * kStride;
-    auto partial = [&](int k) { return base + slot_of(f.first + k, f.first) * slot_floats; };
-    float m = -1e30f;
-    for (int k = lane; k < n; k += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(partial(k));
-      if (ml.y != 0.f) m = fmaxf(m, ml.x);
+  const int nrows = min(RT, T * a.g.G - f.tile * RT), n = f.last - first + 1;
+  const int v0 = blockIdx.y * kRows, r = threadIdx.x & (kRows - 1), c0 = threadIdx.x / kRows, v = v0 + r;
+  if (v0 >= nrows) return;
+  auto part = [&](int k) { return part_of<D>(a.wk.part, slot_of(first + k, first), RT); };
+  float m = -1e30f, l = 0.f;
+  float4 o[C4 / kLanes];
+#pragma unroll
+  for (int i = 0; i < C4 / kLanes; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (v < nrows) {
+    for (int k = 0; k < n; ++k) {
+      const float2 x = reinterpret_cast<const float2*>(part(k))[v];
+      if (x.y != 0.f) m = fmaxf(m, x.x);      // a partial that saw nothing has l = 0
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, o[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = 0.f;
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
-      const float2 ml = *reinterpret_cast<const float2*>(partial(k));
-      const float w = ml.y == 0.f ? 0.f : ex2(ml.x - m);
-      float r[C];
-      if constexpr (C == 4) {
-        const float4 t = *reinterpret_cast<const float4*>(partial(k) + 4 + 4 * lane);
-        r[0] = t.x; r[1] = t.y; r[2] = t.z; r[3] = t.w;
-      } else {
-        const float2 t = *reinterpret_cast<const float2*>(partial(k) + 4 + 2 * lane);
-        r[0] = t.x; r[1] = t.y;
+      const float* p = part(k);
+      const float2 x = reinterpret_cast<const float2*>(p)[v];
+      const float w = x.y == 0.f ? 0.f : ex2(x.x - m);
+      l = fmaf(x.y, w, l);
+#pragma unroll
+      for (int i = 0; i < C4 / kLanes; ++i) {
+        const float4 t = reinterpret_cast<const float4*>(p + 2 * RT)[(c0 + i * kLanes) * RT + v];
+        o[i].x = fmaf(t.x, w, o[i].x);
+        o[i].y = fmaf(t.y, w, o[i].y);
+        o[i].z = fmaf(t.z, w, o[i].z);
+        o[i].w = fmaf(t.w, w, o[i].w);
       }
-      l = fmaf(ml.y, w, l);
-#pragma unroll
-      for (int i = 0; i < C; ++i) o[i] = fmaf(r[i], w, o[i]);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int row = f.tile * RT + v, j = row / a.g.G, hg = row - j * a.g.G;
-    uint16_t* dst = a.out + static_cast<long long>(start + j) * a.out_ts + (f.h * a.g.G + hg) * a.out_hs + C * lane;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int i = 0; i < C; i += 2) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(o[i] * inv, o[i + 1] * inv);
-      *reinterpret_cast<__nv_bfloat162*>(dst + i) = h;
-    }
+  for (int i = 0; i < C4 / kLanes; ++i) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(o[i].x * inv, o[i].y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(o[i].z * inv, o[i].w * inv);
+    float2 pk;
+    memcpy(&pk.x, &lo, 4);
+    memcpy(&pk.y, &hi, 4);
+    out_tile[r][c0 + i * kLanes] = pk;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kRows * C4; i += kThreads) {
+    const int rr = i / C4, c = i - rr * C4;
+    if (v0 + rr >= nrows) break;
+    const int row = f.tile * RT + v0 + rr, j = row / a.g.G, hg = row - j * a.g.G;
+    uint16_t* dst = a.out + static_cast<long long>(start + j) * a.out_ts + (f.h * a.g.G + hg) * a.out_hs;
+    reinterpret_cast<float2*>(dst)[c] = out_tile[rr][c];
   }
 }
 
@@ -582,37 +590,34 @@ static int tile_rows(const Geo& g, const Batch& bt) {
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
 }
 
-struct WorkLayout {
-  long long units;
-  size_t info, part, total;
-};
+static int most_ctas(int rt) { return rt > 16 ? kMaxChunkCtas : kMaxCtas; }
 
-static WorkLayout work_layout(const Geo& g, const Batch& bt, int rt) {
-  WorkLayout w;
-  w.units = max_units(g, bt, rt);
-  w.info = 256;
-  w.part = w.info + (w.units * sizeof(UnitInfo) + 255) / 256 * 256;
-  w.total = w.part + 2 * static_cast<size_t>(rt > 16 ? kMaxChunkCtas : kMaxCtas) * rt * part_stride(g.D) * sizeof(float);
-  return w;
+// First the notes on shared units, then the partials, and the plans of the tcgen05 kernel.
+static size_t info_bytes(int rt) { return (most_ctas(rt) * sizeof(UnitInfo) + 255) / 256 * 256; }
+
+static size_t part_bytes(const Geo& g, int rt) { return 2 * most_ctas(rt) * part_floats(g.D, rt) * sizeof(float); }
+
+size_t attention_workspace_bytes(const Geo& g, const Batch& bt) {
+  const int rt = tile_rows(g, bt);
+  return info_bytes(rt) + part_bytes(g, rt) + (rt > 16 ? kMaxChunkCtas * plan_bytes(bt.B) : 0);
 }
 
-size_t attention_workspace_bytes(const Geo& g, const Batch& bt) { return work_layout(g, bt, tile_rows(g, bt)).total; }
-
 template <int D, int NT>
-static cudaError_t launch_rows(AttnArgs& a, cudaStream_t s) {
+static cudaError_t launch_rows(const AttnArgs& a, int* ctas, cudaStream_t s) {
   const size_t smem = kWarps * kStages * 40 * D + plan_bytes(a.bt.B);
   int wave = 0;
   const cudaError_t e = wave_of<D, NT>(smem, &wave);
   if (e != cudaSuccess) return e;
-  decode_kernel<D, NT><<<wave < kMaxCtas ? wave : kMaxCtas, kThreads, smem, s>>>(a);
+  *ctas = wave < kMaxCtas ? wave : kMaxCtas;
+  decode_kernel<D, NT><<<*ctas, kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
 template <int D>
-static cudaError_t launch_merge(const AttnArgs& a, long long units, int rt, cudaStream_t s) {
+static cudaError_t launch_merge(const AttnArgs& a, int ctas, int rt, cudaStream_t s) {
   // the merge is resident early and waits for the partials (griddepcontrol)
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units), rt == 8 ? 1 : rt == 16 ? 2 : 8);
+  cfg.gridDim = dim3(ctas, rt / 8);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr;
@@ -626,7 +631,6 @@ static cudaError_t launch_merge(const AttnArgs& a, long long units, int rt, cuda
 cudaError_t launch_attention(const Geo& g, const Batch& bt, const pnmix_rows& q, const pnmix_rows& out, void* ws,
                              cudaStream_t s) {
   const int rt = tile_rows(g, bt);
-  const WorkLayout w = work_layout(g, bt, rt);
   AttnArgs a{};
   a.g = g;
   a.bt = bt;
@@ -634,20 +638,19 @@ cudaError_t launch_attention(const Geo& g, const Batch& bt, const pnmix_rows& q,
   a.out = out.data;
   a.out_ts = out.token_stride;
   a.out_hs = out.head_stride;
-  a.lead = 384;
-  char* base = static_cast<char*>(ws);
-  a.wk.count = reinterpret_cast<int*>(base);
-  a.wk.info = reinterpret_cast<UnitInfo*>(base + w.info);
-  a.wk.part = reinterpret_cast<float*>(base + w.part);
+  a.grain = {384, 128};
+  a.wk.info = static_cast<UnitInfo*>(ws);
+  a.wk.part = reinterpret_cast<float*>(static_cast<char*>(ws) + info_bytes(rt));
+  int ctas = 0;
   cudaError_t e;
   if (rt > 16)
-    e = launch_chunk(g, bt, a.q, out, a.wk, rt, s);
+    e = launch_chunk(g, bt, a.q, out, a.wk, reinterpret_cast<uint8_t*>(a.wk.part) + part_bytes(g, rt), rt, &ctas, s);
   else if (g.D == 64)
-    e = rt == 8 ? launch_rows<64, 1>(a, s) : launch_rows<64, 2>(a, s);
+    e = rt == 8 ? launch_rows<64, 1>(a, &ctas, s) : launch_rows<64, 2>(a, &ctas, s);
   else
-    e = rt == 8 ? launch_rows<128, 1>(a, s) : launch_rows<128, 2>(a, s);
+    e = rt == 8 ? launch_rows<128, 1>(a, &ctas, s) : launch_rows<128, 2>(a, &ctas, s);
   if (e != cudaSuccess) return e;
-  return g.D == 64 ? launch_merge<64>(a, w.units, rt, s) : launch_merge<128>(a, w.units, rt, s);
+  return g.D == 64 ? launch_merge<64>(a, ctas, rt, s) : launch_merge<128>(a, ctas, rt, s);
 }
 
 }  // namespace kv4

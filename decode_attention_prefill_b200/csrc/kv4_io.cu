@@ -2,14 +2,19 @@
 // queries and keys, the quantised write (alone or fused behind the rotation) and the
 // read-back.  One kernel for the first two, one for the last.
 //
-// All three move bytes: a bf16 row of 128 channels is 256 bytes and its packed form 80, the
-// arithmetic is a few tens of instructions per 8 channels, so device memory bounds long
-// inputs and latency the decode step.  A head's row is held by D / 8 lanes, 8 channels (one
-// 16-byte load) each: the norm's sum, the group's minimum and maximum and the rotation's
-// partner channels are shuffles inside the row, and nothing but the angles passes through
-// shared memory.  A CTA takes a few tokens and all their heads, so a token's angles (fp64
-// product, reduced to a turn, one sincospi per pair) and its place in the cache are worked
-// out once per CTA, while the first rows' loads are in flight.
+// All three move bytes: a bf16 row of 128 channels is 256 bytes and its packed form 80, so
+// device memory bounds long inputs, closely followed by the instructions (7 to 10 a channel),
+// and latency the decode step.  Four lanes hold a head's row, lane w the channels 8w .. 8w + 7
+// of every group of 32: then the norm's sum and a group's minimum and maximum are two
+// shuffles, the partner channels of a whole-head rotation (D / 2 away, D / 64 groups) are in
+// the same lane, and a lane's codes are one key piece or two neighbouring value pieces, each
+// one store.  (With D / 8 lanes of 8 channels, the first form, every row took eight more
+// shuffles and narrow stores: 123 us instead of NORM_US for 16384 tokens of 40 heads, and the
+// read-back, with integer conversions at a quarter of the rate, 96 us instead of READ_US for
+// 2 x 32768 tokens of 8 heads.)  A warp's eight rows are eight tokens of a head where there are
+// that many: their packed rows lie side by side.  A token's angles (fp64 product, reduced to a
+// turn, one sincospi per pair) and its place in the cache are worked out once per CTA, while
+// the first rows' loads are in flight; the next row's loads are issued before a row is worked on.
 #include "kv4.cuh"
 #include "kv4_launch.cuh"
 
@@ -17,9 +22,9 @@ namespace pnmix {
 namespace kv4 {
 namespace {
 
-constexpr int kIoThreads = 256;
-constexpr int kMaxTok = 16;       // tokens per CTA at most
-constexpr int kAhead = 4;         // rows a lane group loads before it works on the first
+constexpr int kIoThreads = 128;
+constexpr int kRowsPass = kIoThreads / 4;   // rows a CTA works on at once
+constexpr int kMaxTok = 16;                 // tokens per CTA at most
 
 // Sequence of packed row `row`: the last b with q_start[b] <= row, or -1 for a row outside
 // every sequence.  Called by a whole warp.
@@ -63,7 +68,7 @@ __device__ __forceinline__ void row_place(const Geo& g, const Batch& bt, int row
   tok = inside & 15;
 }
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(uint4 v, float* x) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -72,7 +77,7 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
   }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+__device__ __forceinline__ uint4 pack8(const float* x) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -82,13 +87,59 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Between lanes l and l ^ 4 (neighbouring channel groups of a row): a lane's eight codes
-// (its low half one value piece, its high half the next) against the stored words, which
-// hold one piece of both groups.  The exchange is its own inverse.
-__device__ __forceinline__ uint32_t cross_groups(uint32_t w, bool odd) {
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? (w & 0xFFFFu) : (w >> 16), 4);
-  return odd ? (other | (w & 0xFFFF0000u)) : ((w & 0xFFFFu) | (other << 16));
+// Minimum / maximum that return NaN if either is one.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// n words (2 or 4) as one access.
+template <int N>
+__device__ __forceinline__ void put_words(uint8_t* p, const uint32_t (&w)[N]) {
+  if constexpr (N == 4)
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+template <int N>
+__device__ __forceinline__ void get_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  }
+}
+
+// A lane's codes (word g: eight channels of group g) <-> its two neighbouring value pieces (a
+// piece has four channels of every group, 16 bits each).
+template <int NG>
+__device__ __forceinline__ void to_pieces(const uint32_t (&w)[NG], uint32_t (&p)[NG]) {
+#pragma unroll
+  for (int i = 0; i < NG / 2; ++i) {
+    p[i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x5410);
+    p[NG / 2 + i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);
+  }
+}
+template <int NG>
+__device__ __forceinline__ void from_pieces(const uint32_t (&p)[NG], uint32_t (&w)[NG]) {
+#pragma unroll
+  for (int i = 0; i < NG / 2; ++i) {
+    w[2 * i] = __byte_perm(p[i], p[NG / 2 + i], 0x5410);
+    w[2 * i + 1] = __byte_perm(p[i], p[NG / 2 + i], 0x7632);
+  }
+}
+
+// How the rotation finds a channel's partner: in the same lane (pairs D / 2 apart), next to it
+// (interleaved), or through shared memory (any other distance).
+enum { kHalves = 0, kNext = 1, kAnywhere = 2 };
 
 struct IoArgs {
   Geo g;
@@ -106,16 +157,20 @@ struct IoArgs {
   const int32_t* positions;
 };
 
-// L: lanes of a row (head_dim / 8).  ROPE: q and k rows are normed and rotated.  QUANT: k and
-// v rows go to the cache (otherwise k rows are stored like q's).
-template <int L, bool ROPE, bool QUANT>
+// Floats of a token's angles in shared memory: cos, sin, and a step of 16 bytes so that the
+// eight tokens of a warp meet in no bank.
+__host__ __device__ __forceinline__ int turn_stride(int half) { return 2 * half + 4; }
+
+// ROPE: q and k rows are normed and rotated.  QUANT: k and v rows go to the cache (otherwise
+// k rows are stored like q's).
+template <int D, bool ROPE, bool QUANT, int PAIRS>
 __global__ void __launch_bounds__(kIoThreads)
 rows_in_kernel(const __grid_constant__ IoArgs a) {
-  constexpr int D = 8 * L, kRows = kIoThreads / L, kGroups = D / 32;
-  extern __shared__ float turn[];             // [token][cos, sin][rot / 2]
+  constexpr int NG = D / 32;
+  extern __shared__ __align__(16) float shared[];   // [token][cos, sin], then [warp][8 rows][D + 4]
   __shared__ long long place[kMaxTok];
   __shared__ int place_tok[kMaxTok];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = tid & (L - 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, w = lane & 3;
   const int ntok = 1 << a.tok_shift, tok0 = blockIdx.x << a.tok_shift;
   const int total = (a.nq + a.nk + a.nv) << a.tok_shift;   // rows of this CTA, tokens inner
   const int half = a.rope.rot_dim >> 1;
@@ -131,18 +186,23 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
     head -= a.nk;
     return 2;
   };
-  auto load = [&](int rho) {
+  auto load = [&](int rho, uint4 (&v)[NG]) {
     int t, head;
     const int kind = find(rho, t, head);
-    if (kind < 0) return make_uint4(0u, 0u, 0u, 0u);
+    if (kind < 0) {
+#pragma unroll
+      for (int k = 0; k < NG; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
+      return;
+    }
     const Rows& r = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    return *(reinterpret_cast<const uint4*>(r.p + (tok0 + t) * r.ts + head * r.hs) + l);
+    const uint4* src = reinterpret_cast<const uint4*>(r.p + (tok0 + t) * r.ts + head * r.hs) + w;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) v[k] = src[4 * k];
   };
 
-  uint4 buf[kAhead];
-  const int mine = tid / L;
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u) buf[u] = load(u * kRows + mine);
+  uint4 next[NG];
+  const int mine = tid >> 2;
+  load(mine, next);
 
   if (QUANT) {
     for (int i = warp; i < ntok; i += kIoThreads / 32) {
@@ -168,126 +228,171 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
         turns -= rint(turns);
         sincospif(2.f * static_cast<float>(turns), &s, &c);
       }
-      turn[(2 * t) * half + p] = c;
-      turn[(2 * t + 1) * half + p] = s;
+      shared[t * turn_stride(half) + p] = c;
+      shared[t * turn_stride(half) + half + p] = s;
     }
   }
-  __syncthreads();
+  if (ROPE || QUANT) __syncthreads();
 
-  for (int rho0 = mine; rho0 - mine < total; rho0 += kAhead * kRows) {
-    if (rho0 != mine) {
+  for (int rho = mine; rho - mine < total; rho += kRowsPass) {
+    float x[8 * NG];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) buf[u] = load(rho0 + u * kRows);
-    }
+    for (int k = 0; k < NG; ++k) unpack8(next[k], x + 8 * k);
+    if (rho - mine + kRowsPass < total) load(rho + kRowsPass, next);
+    int t, head;
+    const int kind = find(rho, t, head);
+    if (ROPE && __any_sync(0xffffffffu, kind == 0 || kind == 1)) {
+      // value rows in the same warp go through it too, as rows without a rotation
+      const bool turns = kind == 0 || kind == 1;
+      const uint16_t* wt = kind == 0 ? a.qw : a.kw;
+      float ss = 0.f;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (rho0 - mine + u * kRows >= total) break;   // the same for the whole CTA
-      int t, head;
-      const int kind = find(rho0 + u * kRows, t, head);
-      float x[8];
-      unpack8(buf[u], x);
-      if (ROPE) {   // every lane takes part in the shuffles; value rows keep x
-        float y[8];
-        const uint16_t* w = kind == 0 ? a.qw : a.kw;
-        float ss = 0.f;
+      for (int i = 0; i < 8 * NG; ++i) ss = fmaf(x[i], x[i], ss);
+      ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+      ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+      if (wt && turns) {
+        const float r = rsqrtf(ss * (1.0f / D) + a.rope.eps);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (w && kind >= 0 && kind < 2) {
-          const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.rope.eps);
+        for (int k = 0; k < NG; ++k) {
           float wf[8];
-          unpack8(__ldg(reinterpret_cast<const uint4*>(w) + l), wf);
+          unpack8(__ldg(reinterpret_cast<const uint4*>(wt) + 4 * k + w), wf);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[i] * r * wf[i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[i];
+          for (int i = 0; i < 8; ++i) x[8 * k + i] *= r * wf[i];
         }
-        const float* cs = turn + (2 * t) * half;
-        if (a.rope.interleaved) {
-          if (8 * l < a.rope.rot_dim) {
-            const float4 c = *reinterpret_cast<const float4*>(cs + 4 * l);
-            const float4 s = *reinterpret_cast<const float4*>(cs + half + 4 * l);
-            const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+      }
+      const float* cs = shared + t * turn_stride(half);
+      if constexpr (PAIRS == kHalves) {
+        if (turns) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float p = y[2 * i], q = y[2 * i + 1];
-              y[2 * i] = p * cc[i] - q * sn[i];
-              y[2 * i + 1] = q * cc[i] + p * sn[i];
+          for (int k = 0; k < NG / 2; ++k) {
+            float c[8], s[8];
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+              *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(cs + 32 * k + 8 * w + i);
+              *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(cs + half + 32 * k + 8 * w + i);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float &p = x[8 * k + i], &q = x[8 * (k + NG / 2) + i];
+              const float p0 = p;
+              p = p0 * c[i] - q * s[i];
+              q = q * c[i] + p0 * s[i];
             }
           }
-        } else {
-          const int hl = half >> 3;   // lanes of a row's first half
-          const bool first = l < hl, turned = l < 2 * hl;
-          const int base = first ? l : l - hl;
-          const int src = turned ? (first ? l + hl : l - hl) : l;
-          float o[8];
+        }
+      } else if constexpr (PAIRS == kNext) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, y[i], src, L);
-          if (turned) {
-            const float4 c0 = *reinterpret_cast<const float4*>(cs + 8 * base);
-            const float4 c1 = *reinterpret_cast<const float4*>(cs + 8 * base + 4);
-            const float4 s0 = *reinterpret_cast<const float4*>(cs + half + 8 * base);
-            const float4 s1 = *reinterpret_cast<const float4*>(cs + half + 8 * base + 4);
-            const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-            const float sn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        for (int k = 0; k < NG; ++k) {
+          if (turns && 32 * k + 8 * w < a.rope.rot_dim) {
+            float c[4], s[4];
+            *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(cs + 16 * k + 4 * w);
+            *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(cs + half + 16 * k + 4 * w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = first ? y[i] * cc[i] - o[i] * sn[i] : y[i] * cc[i] + o[i] * sn[i];
+            for (int i = 0; i < 4; ++i) {
+              float &p = x[8 * k + 2 * i], &q = x[8 * k + 2 * i + 1];
+              const float p0 = p;
+              p = p0 * c[i] - q * s[i];
+              q = q * c[i] + p0 * s[i];
+            }
           }
         }
-        if (kind >= 0 && kind < 2) {
+      } else {
+        float* row = shared + (turn_stride(half) << a.tok_shift) + (warp * 8 + (lane >> 2)) * (D + 4);
+        __syncwarp();   // the rows before were read
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = y[i];
+        for (int i = 0; i < 8 * NG; i += 4)
+          *reinterpret_cast<float4*>(row + 32 * (i >> 3) + 8 * w + (i & 7)) = *reinterpret_cast<float4*>(x + i);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+          const int ch = 32 * k + 8 * w;
+          if (turns && ch < a.rope.rot_dim) {
+            const bool first = ch < half;
+            const int p = first ? ch : ch - half;
+            const float* other = row + (first ? ch + half : ch - half);
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+              const float4 o = *reinterpret_cast<const float4*>(other + i);
+              const float4 c = *reinterpret_cast<const float4*>(cs + p + i);
+              float4 s = *reinterpret_cast<const float4*>(cs + half + p + i);
+              if (first) s = make_float4(-s.x, -s.y, -s.z, -s.w);
+              float* y = x + 8 * k + i;
+              y[0] = y[0] * c.x + o.x * s.x;
+              y[1] = y[1] * c.y + o.y * s.y;
+              y[2] = y[2] * c.z + o.z * s.z;
+              y[3] = y[3] * c.w + o.w * s.w;
+            }
+          }
         }
-        if (kind == 0 && (!QUANT || place[t] != -2))
-          *(reinterpret_cast<uint4*>(a.qo + (tok0 + t) * a.qo_ts + head * a.qo_hs) + l) = pack8(x);
-        if (!QUANT && kind == 1)
-          *(reinterpret_cast<uint4*>(a.ko + (tok0 + t) * a.ko_ts + head * a.ko_hs) + l) = pack8(x);
-        if (QUANT) unpack8(pack8(x), x);   // keys enter the cache as the bf16 row a separate call would write
       }
-      if constexpr (QUANT) {
-        bool odd_number = false;
+      uint4 b[NG];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          odd_number |= !(fabsf(x[i]) <= kLimit);
-          x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -kLimit), kLimit) : 0.f;
-        }
-        float mn = x[0], mx = x[0];
+      for (int k = 0; k < NG; ++k) b[k] = pack8(x + 8 * k);
+      if ((kind == 0 && (!QUANT || place[t] != -2)) || (!QUANT && kind == 1)) {
+        uint16_t* dst = kind == 0 ? a.qo + (tok0 + t) * a.qo_ts + head * a.qo_hs
+                                  : a.ko + (tok0 + t) * a.ko_ts + head * a.ko_hs;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) {
-          mn = fminf(mn, x[i]);
-          mx = fmaxf(mx, x[i]);
-        }
+        for (int k = 0; k < NG; ++k) reinterpret_cast<uint4*>(dst)[4 * k + w] = b[k];
+      }
+      if (QUANT) {   // keys enter the cache as the bf16 row a separate call would write
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        for (int k = 0; k < NG; ++k) unpack8(b[k], x + 8 * k);
+      }
+    }
+    if constexpr (QUANT) {
+      if (!__any_sync(0xffffffffu, kind > 0)) continue;
+      float mn[NG], mx[NG];
+      auto range = [&]() {
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+          mn[k] = mx[k] = x[8 * k];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) {
+            mn[k] = min_nan(mn[k], x[8 * k + i]);
+            mx[k] = max_nan(mx[k], x[8 * k + i]);
+          }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            mn[k] = min_nan(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], o));
+            mx[k] = max_nan(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+          }
         }
-        const QParams qp = quant_params(mn, mx, 4);
-        uint32_t w = 0u;
+      };
+      range();
+      bool odd = false;
+#pragma unroll
+      for (int k = 0; k < NG; ++k) odd |= !(mn[k] >= -kLimit && mx[k] <= kLimit);
+      if (__any_sync(0xffffffffu, odd)) {   // a NaN or a number past the limit: taken inside
+#pragma unroll
+        for (int i = 0; i < 8 * NG; ++i) x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -kLimit), kLimit) : 0.f;
+        range();
+      }
+      uint32_t code[NG], sz[NG];
+#pragma unroll
+      for (int k = 0; k < NG; ++k) {
+        const QParams qp = quant_params(mn[k], mx[k], 4);
+        code[k] = 0u;
         if (qp.s != 0.f) {
           const float inv = __frcp_rn(qp.s);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w |= quant_code_rcp(x[i], qp.z, qp.s, inv, 15) << (4 * i);
+          for (int i = 0; i < 8; ++i) code[k] |= quant_code_rcp(x[8 * k + i], qp.z, qp.s, inv, 15) << (4 * i);
         }
-        const int grp = l >> 2, piece = l & 3;
-        const uint32_t crossed = cross_groups(w, grp & 1);
-        if (kind > 0 && place[t] >= 0) {
-          const int tok = place_tok[t];
-          uint8_t* blk = a.g.pages + place[t] + static_cast<size_t>(head) * ((1 << (a.g.page_shift - 4)) * block_bytes(D)) +
-                         (kind == 2 ? 10 * D : 0);
-          uint8_t* row = blk + tok * (D / 2);
-          if (kind == 1)
-            *reinterpret_cast<uint32_t*>(row + piece * (4 * kGroups) + grp * 4) = w;
-          else
-            *reinterpret_cast<uint32_t*>(row + value_place<D>(tok, 2 * piece + (grp & 1)) * (2 * kGroups) +
-                                         (grp >> 1) * 4) = crossed;
-          if (piece == 0)
-            *reinterpret_cast<uint32_t*>(blk + 8 * D + tok * (4 * kGroups) + grp * 4) =
-                static_cast<uint32_t>(qp.s16) | (static_cast<uint32_t>(qp.z16) << 16);
-          if (odd_number) raise(a.g.error, PNMIX_DEVERR_NONFINITE);
+        sz[k] = static_cast<uint32_t>(qp.s16) | (static_cast<uint32_t>(qp.z16) << 16);
+      }
+      if (kind > 0 && place[t] >= 0) {
+        const int tok = place_tok[t];
+        uint8_t* blk = a.g.pages + place[t] + static_cast<size_t>(head) * ((1 << (a.g.page_shift - 4)) * block_bytes(D)) +
+                       (kind == 2 ? 10 * D : 0);
+        uint8_t* row = blk + tok * (D / 2);
+        if (kind == 1) {
+          put_words<NG>(row + w * (4 * NG), code);
+        } else {
+          uint32_t p[NG];
+          to_pieces<NG>(code, p);
+          put_words<NG>(row + value_place<D>(tok, 2 * w) * (2 * NG), p);
         }
+        if (w == 0) put_words<NG>(blk + 8 * D + tok * (4 * NG), sz);
+        if (odd) raise(a.g.error, PNMIX_DEVERR_NONFINITE);
       }
     }
   }
@@ -302,13 +407,13 @@ struct OutArgs {
   long long k_ts, k_hs, v_ts, v_hs;
 };
 
-template <int L>
+template <int D>
 __global__ void __launch_bounds__(kIoThreads)
 rows_out_kernel(const __grid_constant__ OutArgs a) {
-  constexpr int D = 8 * L, kRows = kIoThreads / L, kGroups = D / 32;
+  constexpr int NG = D / 32, kAhead = 2;
   __shared__ long long place[kMaxTok];
   __shared__ int place_tok[kMaxTok];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = tid & (L - 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, w = lane & 3;
   const int ntok = 1 << a.tok_shift, tok0 = blockIdx.x << a.tok_shift;
   const int row0 = blockIdx.y * a.rows_y, rows = min(a.rows_y, 2 * a.g.Hkv - row0);
   const int total = rows << a.tok_shift;
@@ -322,57 +427,83 @@ rows_out_kernel(const __grid_constant__ OutArgs a) {
     }
   }
   __syncthreads();
-  const int grp = l >> 2, piece = l & 3;
   const size_t head_bytes = static_cast<size_t>(1 << (a.g.page_shift - 4)) * block_bytes(D);
-  for (int rho0 = tid / L; rho0 - static_cast<int>(tid / L) < total; rho0 += kAhead * kRows) {
-    uint32_t w[kAhead], sz[kAhead];
+  for (int rho0 = tid >> 2; rho0 < total; rho0 += kAhead * kRowsPass) {
+    uint32_t code[kAhead][NG], sz[kAhead][NG];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int rho = rho0 + u * kRows, t = rho & (ntok - 1), r = row0 + (rho >> a.tok_shift);
-      w[u] = sz[u] = 0u;
+      const int rho = rho0 + u * kRowsPass, t = rho & (ntok - 1), r = row0 + (rho >> a.tok_shift);
+#pragma unroll
+      for (int k = 0; k < NG; ++k) code[u][k] = sz[u][k] = 0u;
       if (rho < total && place[t] >= 0) {
-        const int tok = place_tok[t], head = r >> 1;
-        const uint8_t* blk = a.g.pages + place[t] + head * head_bytes + ((r & 1) ? 10 * D : 0);
+        const int tok = place_tok[t];
+        const uint8_t* blk = a.g.pages + place[t] + (r >> 1) * head_bytes + ((r & 1) ? 10 * D : 0);
         const uint8_t* row = blk + tok * (D / 2);
-        w[u] = *reinterpret_cast<const uint32_t*>(
-            (r & 1) ? row + value_place<D>(tok, 2 * piece + (grp & 1)) * (2 * kGroups) + (grp >> 1) * 4
-                    : row + piece * (4 * kGroups) + grp * 4);
-        sz[u] = *reinterpret_cast<const uint32_t*>(blk + 8 * D + tok * (4 * kGroups) + grp * 4);
+        get_words<NG>((r & 1) ? row + value_place<D>(tok, 2 * w) * (2 * NG) : row + w * (4 * NG), code[u]);
+        get_words<NG>(blk + 8 * D + tok * (4 * NG), sz[u]);
       }
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int rho = rho0 + u * kRows, t = rho & (ntok - 1), r = row0 + (rho >> a.tok_shift);
-      const uint32_t crossed = cross_groups(w[u], grp & 1);   // every lane takes part
+      const int rho = rho0 + u * kRowsPass, t = rho & (ntok - 1), r = row0 + (rho >> a.tok_shift);
       if (rho >= total || place[t] == -2) continue;
-      const uint32_t c = (r & 1) ? crossed : w[u];
-      const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(sz[u] & 0xFFFFu)));
-      const float z = __half2float(__ushort_as_half(static_cast<uint16_t>(sz[u] >> 16)));
-      float x[8];
+      if (r & 1) {
+        uint32_t c[NG];
+        from_pieces<NG>(code[u], c);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fmaf(static_cast<float>((c >> (4 * i)) & 15u), s, z);   // c * s is exact
+        for (int k = 0; k < NG; ++k) code[u][k] = c[k];
+      }
       const int head = r >> 1;
       uint16_t* dst = (r & 1) ? a.v + (tok0 + t) * a.v_ts + head * a.v_hs : a.k + (tok0 + t) * a.k_ts + head * a.k_hs;
-      *(reinterpret_cast<uint4*>(dst) + l) = pack8(x);
+#pragma unroll
+      for (int k = 0; k < NG; ++k) {
+        const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(sz[u][k] & 0xFFFFu)));
+        const float z = __half2float(__ushort_as_half(static_cast<uint16_t>(sz[u][k] >> 16)));
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // channels i and i + 4: 1024 + c is an fp16 with c in its low mantissa bits
+          const uint32_t pair = ((code[u][k] >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
+          __half2 h;
+          memcpy(&h, &pair, 4);
+          const float2 c = __half22float2(__hsub2(h, __float2half2_rn(1024.f)));
+          x[i] = fmaf(c.x, s, z);       // c * s is exact
+          x[i + 4] = fmaf(c.y, s, z);
+        }
+        reinterpret_cast<uint4*>(dst)[4 * k + w] = pack8(x);
+      }
     }
   }
 }
 
-// Tokens per CTA: enough that a CTA's rows keep its loads busy, few enough that the grid
-// covers the GPU (8 CTAs of 256 threads fit an SM).
-int token_shift(int n_tokens, int rows, int most) {
-  int s = 0;
-  while (s < most && (rows << s) < 64 && (n_tokens >> (s + 1)) >= 2 * 148) ++s;
+// Tokens per CTA: eight make a warp's rows neighbours in the cache; fewer while the grid would
+// not fill the GPU.
+int token_shift(int n_tokens) {
+  int s = 3;
+  while (s > 0 && (n_tokens >> s) < 4 * 148) --s;
   return s;
 }
 
-template <int L, bool ROPE, bool QUANT>
-cudaError_t launch_in(IoArgs& a, cudaStream_t s) {
-  a.tok_shift = token_shift(a.n_tokens, a.nq + a.nk + a.nv, 4);
+template <int D, bool ROPE, bool QUANT, int PAIRS>
+cudaError_t launch_pairs(const IoArgs& a, cudaStream_t s) {
   const int ctas = (a.n_tokens + (1 << a.tok_shift) - 1) >> a.tok_shift;
-  const size_t smem = ROPE ? sizeof(float) * a.rope.rot_dim << a.tok_shift : 0;
-  rows_in_kernel<L, ROPE, QUANT><<<ctas, kIoThreads, smem, s>>>(a);
+  size_t floats = 0;
+  if (ROPE) floats += static_cast<size_t>(turn_stride(a.rope.rot_dim >> 1)) << a.tok_shift;
+  if (ROPE && PAIRS == kAnywhere) floats += kIoThreads / 4 * (D + 4);
+  rows_in_kernel<D, ROPE, QUANT, PAIRS><<<ctas, kIoThreads, floats * sizeof(float), s>>>(a);
   return cudaGetLastError();
+}
+
+template <int D, bool ROPE, bool QUANT>
+cudaError_t launch_in(IoArgs& a, cudaStream_t s) {
+  a.tok_shift = token_shift(a.n_tokens);
+  if constexpr (!ROPE) {
+    return launch_pairs<D, ROPE, QUANT, kHalves>(a, s);
+  } else {
+    if (a.rope.interleaved) return launch_pairs<D, ROPE, QUANT, kNext>(a, s);
+    if (a.rope.rot_dim == D) return launch_pairs<D, ROPE, QUANT, kHalves>(a, s);
+    return launch_pairs<D, ROPE, QUANT, kAnywhere>(a, s);
+  }
 }
 
 }  // namespace
@@ -397,9 +528,9 @@ cudaError_t launch_norm_rope(const pnmix_rope& rope, int n_tokens, int nq, int n
   a.kw = kw;
   a.positions = positions;
   switch (rope.head_dim) {
-    case 64: return launch_in<8, true, false>(a, s);
-    case 128: return launch_in<16, true, false>(a, s);
-    default: return launch_in<32, true, false>(a, s);
+    case 64: return launch_in<64, true, false>(a, s);
+    case 128: return launch_in<128, true, false>(a, s);
+    default: return launch_in<256, true, false>(a, s);
   }
 }
 
@@ -411,7 +542,7 @@ cudaError_t launch_append(const Geo& g, const Batch& bt, const pnmix_rows& k, co
   a.nk = a.nv = g.Hkv;
   a.k = {k.data, k.token_stride, k.head_stride};
   a.v = {v.data, v.token_stride, v.head_stride};
-  return g.D == 64 ? launch_in<8, false, true>(a, s) : launch_in<16, false, true>(a, s);
+  return g.D == 64 ? launch_in<64, false, true>(a, s) : launch_in<128, false, true>(a, s);
 }
 
 cudaError_t launch_append_qkv(const Geo& g, const Batch& bt, const pnmix_rope& rope, const pnmix_rows& q,
@@ -433,7 +564,7 @@ cudaError_t launch_append_qkv(const Geo& g, const Batch& bt, const pnmix_rope& r
   a.qw = qw;
   a.kw = kw;
   a.positions = positions;
-  return g.D == 64 ? launch_in<8, true, true>(a, s) : launch_in<16, true, true>(a, s);
+  return g.D == 64 ? launch_in<64, true, true>(a, s) : launch_in<128, true, true>(a, s);
 }
 
 cudaError_t launch_read(const Geo& g, const Batch& bt, const pnmix_rows& k, const pnmix_rows& v, cudaStream_t s) {
@@ -449,15 +580,14 @@ cudaError_t launch_read(const Geo& g, const Batch& bt, const pnmix_rows& k, cons
   // tokens inner: the rows of a block lie together; few tokens leave room for more CTAs in y
   a.tok_shift = 4;
   while (a.tok_shift > 0 && (bt.n_tokens >> a.tok_shift) < 148) --a.tok_shift;
-  const int x = (bt.n_tokens + (1 << a.tok_shift) - 1) >> a.tok_shift;
-  const int rows = 2 * g.Hkv, per_pass = kIoThreads / (g.D / 8) * kAhead;   // rows of one round of loads
-  a.rows_y = max(1, per_pass >> a.tok_shift);
+  const int x = (bt.n_tokens + (1 << a.tok_shift) - 1) >> a.tok_shift, rows = 2 * g.Hkv;
+  a.rows_y = max(1, 2 * kRowsPass >> a.tok_shift);
   while (a.rows_y < rows && static_cast<long long>(x) * ((rows + a.rows_y - 1) / a.rows_y) > 148 * 16) a.rows_y *= 2;
   const dim3 grid(x, (rows + a.rows_y - 1) / a.rows_y);
   if (g.D == 64)
-    rows_out_kernel<8><<<grid, kIoThreads, 0, s>>>(a);
+    rows_out_kernel<64><<<grid, kIoThreads, 0, s>>>(a);
   else
-    rows_out_kernel<16><<<grid, kIoThreads, 0, s>>>(a);
+    rows_out_kernel<128><<<grid, kIoThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -14,6 +14,7 @@ device's current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -95,74 +96,66 @@ for _name, (_res, _args) in SIGNATURES.items():
     _fn = getattr(_lib, _name)
     _fn.restype = _res
     _fn.argtypes = _args
+_norm_rope, _byref = _lib.pnmix_norm_rope, ctypes.byref
 
 
-def _rows(t: torch.Tensor, heads: int, dim: int, device, name: str, tokens: int | None = None) -> _Rows:
+def _rows(t: torch.Tensor, shape: tuple, device, name: str) -> _Rows:
+    """Pointer and strides of a bf16 tensor [tokens][heads][head_dim] on `device`."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape and t.device == device:
+        s0, s1, s2 = t.stride()
+        if s2 == 1:
+            return _Rows(t.data_ptr(), s0 if shape[0] > 1 else 0, s1 if shape[1] > 1 else 0)
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or (tokens is not None and t.shape[0] != tokens):
-        raise ValueError(f"{name} must be [{'tokens' if tokens is None else tokens}][{heads}][{dim}], "
-                         f"got {list(t.shape)}")
-    s0, s1, s2 = t.stride()
-    if s2 != 1:
-        raise ValueError(f"{name}: the channels of a head must be contiguous")
-    return _Rows(t.data_ptr(), 0 if t.shape[0] == 1 else s0, 0 if heads == 1 else s1)
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _ints(t: torch.Tensor, shape: tuple, device, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
-        raise TypeError(f"{name} must be an int32 CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be an int32 tensor")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, not on {device}") if t.is_cuda else \
+            TypeError(f"{name} must be a CUDA tensor")
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
     return t.data_ptr()
+
+
+def _positions(t: torch.Tensor, axes: int, n: int, device) -> int:
+    return _ints(t, (n,) if axes == 1 and isinstance(t, torch.Tensor) and t.dim() == 1 else (axes, n), device,
+                 "positions")
 
 
 def _weight(t, dim: int, device, name: str):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
-    if t.device != device or tuple(t.shape) != (dim,) or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 tensor")
+    if t.device != device or t.shape != (dim,) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous [{dim}] on {device}")
     return t.data_ptr()
 
 
-class _On:
-    """The device a call runs on and the stream it goes to; outputs made inside belong to
-    that stream."""
+_SAME = contextlib.nullcontext()
 
-    def __init__(self, device, stream):
-        self.device, self.stream = device, stream
 
-    def __enter__(self):
-        self._prev = None
-        if self.device.index != torch.cuda.current_device():
-            self._prev = torch.cuda.device(self.device)
-            self._prev.__enter__()
-        self._ctx = None
-        if self.stream is None:
-            return torch.cuda.current_stream().cuda_stream
-        s = self.stream
-        if not hasattr(s, "cuda_stream"):
-            s = torch.cuda.ExternalStream(int(s), device=self.device)
-        if s.device != self.device:
-            self.__exit__()
-            raise ValueError(f"stream is on {s.device}, the tensors on {self.device}")
-        self._ctx = torch.cuda.stream(s)
-        self._ctx.__enter__()
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(None, None, None)
-        if self._prev is not None:
-            self._prev.__exit__(None, None, None)
+def _on(device, stream):
+    """(context, raw stream): where a call on `device` goes.  Outputs made inside the context
+    belong to that stream."""
+    if stream is None:
+        # the raw handle: a Stream object around it costs more than the rest of a small call
+        ctx = _SAME if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return ctx, torch._C._cuda_getCurrentRawStream(device.index)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream), stream.cuda_stream
 
 
 def norm_rope(rope: Rope, q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, q_weight=None, k_weight=None,
@@ -171,18 +164,17 @@ def norm_rope(rope: Rope, q: torch.Tensor, k: torch.Tensor, positions: torch.Ten
     q, k bf16 [n][heads][head_dim]; positions int32 [n_axes][n] ([n] with one axis).  Returns
     (q_out, k_out), which may be the inputs themselves."""
     dev, D = q.device, rope.head_dim
-    n, hq, hk = q.shape[0], q.shape[1], k.shape[1]
-    if rope.n_axes == 1 and positions.dim() == 1:
-        positions = positions[None]
-    rq, rk = _rows(q, hq, D, dev, "q"), _rows(k, hk, D, dev, "k", n)
-    pos = _ints(positions, (rope.n_axes, n), dev, "positions")
+    sq, sk = (q.shape[0], q.shape[1], D), (q.shape[0], k.shape[1], D)
+    rq, rk = _rows(q, sq, dev, "q"), _rows(k, sk, dev, "k")
+    pos = _positions(positions, rope.n_axes, sq[0], dev)
     wq, wk = _weight(q_weight, D, dev, "q_weight"), _weight(k_weight, D, dev, "k_weight")
-    with _On(dev, stream) as s:
-        q_out = torch.empty((n, hq, D), dtype=q.dtype, device=dev) if q_out is None else q_out
-        k_out = torch.empty((n, hk, D), dtype=q.dtype, device=dev) if k_out is None else k_out
-        oq, ok = _rows(q_out, hq, D, dev, "q_out", n), _rows(k_out, hk, D, dev, "k_out", n)
-        _check(_lib.pnmix_norm_rope(ctypes.byref(rope), n, hq, hk, ctypes.byref(rq), ctypes.byref(rk), wq, wk, pos,
-                                    ctypes.byref(oq), ctypes.byref(ok), s), "pnmix_norm_rope")
+    ctx, s = _on(dev, stream)
+    with ctx:
+        q_out = q.new_empty(sq) if q_out is None else q_out
+        k_out = k.new_empty(sk) if k_out is None else k_out
+        _check(_norm_rope(_byref(rope), sq[0], sq[1], sk[1], _byref(rq), _byref(rk), wq, wk, pos,
+                          _byref(_rows(q_out, sq, dev, "q_out")), _byref(_rows(k_out, sk, dev, "k_out")), s),
+               "pnmix_norm_rope")
     return q_out, k_out
 
 
@@ -210,6 +202,7 @@ class KV4Batch:
                         None if q_start is None else _ints(q_start, (B + 1,), dev, "q_start"),
                         _ints(kv_len, (B,), dev, "kv_len"),
                         _ints(page_table, (B, page_table.shape[1]), dev, "page_table"))
+        self.ref = ctypes.byref(self.c)
 
 
 class KV4Cache:
@@ -228,56 +221,57 @@ class KV4Cache:
         _check(_lib.pnmix_kv4_cache_init(ctypes.byref(cfg), n_pages, buffer.data_ptr(), buffer.numel(),
                                          ctypes.byref(self.c)), "pnmix_kv4_cache_init")
         self._refs = (ctypes.byref(cfg), ctypes.byref(self.c))
+        self._q, self._kv = (cfg.n_q_heads, cfg.head_dim), (cfg.n_kv_heads, cfg.head_dim)
 
     def reset(self, stream=None):
         """Zero the pages and the error word."""
-        with _On(self.device, stream) as s:
+        ctx, s = _on(self.device, stream)
+        with ctx:
             _check(_lib.pnmix_kv4_cache_reset(self._refs[1], s), "pnmix_kv4_cache_reset")
 
     def _on(self, batch: KV4Batch, stream):
         if batch.device != self.device:
             raise ValueError(f"the batch is on {batch.device}, the cache on {self.device}")
-        return _On(self.device, stream)
+        return _on(self.device, stream)
 
     def append(self, batch: KV4Batch, k: torch.Tensor, v: torch.Tensor, stream=None):
         """Quantise rows k, v bf16 [n][Hkv][head_dim] (after RoPE) into the batch's places."""
-        H, D, n = self.cfg.n_kv_heads, self.cfg.head_dim, batch.n_tokens
-        rk, rv = _rows(k, H, D, self.device, "k", n), _rows(v, H, D, self.device, "v", n)
-        with self._on(batch, stream) as s:
-            _check(_lib.pnmix_kv4_append(self._refs[0], ctypes.byref(batch.c), ctypes.byref(rk), ctypes.byref(rv),
-                                         self._refs[1], s), "pnmix_kv4_append")
+        kv = (batch.n_tokens, *self._kv)
+        rk, rv = _rows(k, kv, self.device, "k"), _rows(v, kv, self.device, "v")
+        ctx, s = self._on(batch, stream)
+        with ctx:
+            _check(_lib.pnmix_kv4_append(self._refs[0], batch.ref, _byref(rk), _byref(rv), self._refs[1], s),
+                   "pnmix_kv4_append")
 
     def append_qkv(self, batch: KV4Batch, rope: Rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                    positions: torch.Tensor, q_weight=None, k_weight=None, q_out: torch.Tensor | None = None,
                    stream=None) -> torch.Tensor:
         """norm_rope of q and k and append of the rotated k and v in one pass; returns q_out."""
-        c, n, dev = self.cfg, batch.n_tokens, self.device
-        D = c.head_dim
-        if rope.n_axes == 1 and positions.dim() == 1:
-            positions = positions[None]
-        rq, rk = _rows(q, c.n_q_heads, D, dev, "q", n), _rows(k, c.n_kv_heads, D, dev, "k", n)
-        rv = _rows(v, c.n_kv_heads, D, dev, "v", n)
-        pos = _ints(positions, (rope.n_axes, n), dev, "positions")
+        n, dev = batch.n_tokens, self.device
+        qs, kv = (n, *self._q), (n, *self._kv)
+        rq, rk, rv = _rows(q, qs, dev, "q"), _rows(k, kv, dev, "k"), _rows(v, kv, dev, "v")
+        pos = _positions(positions, rope.n_axes, n, dev)
+        D = qs[2]
         wq, wk = _weight(q_weight, D, dev, "q_weight"), _weight(k_weight, D, dev, "k_weight")
-        with self._on(batch, stream) as s:
-            if q_out is None:
-                q_out = torch.empty((n, c.n_q_heads, D), dtype=q.dtype, device=dev)
-            ro = _rows(q_out, c.n_q_heads, D, dev, "q_out", n)
-            _check(_lib.pnmix_kv4_append_qkv(self._refs[0], ctypes.byref(rope), ctypes.byref(batch.c),
-                                             ctypes.byref(rq), ctypes.byref(rk), ctypes.byref(rv), wq, wk, pos,
-                                             ctypes.byref(ro), self._refs[1], s), "pnmix_kv4_append_qkv")
+        ctx, s = self._on(batch, stream)
+        with ctx:
+            q_out = q.new_empty(qs) if q_out is None else q_out
+            _check(_lib.pnmix_kv4_append_qkv(self._refs[0], _byref(rope), batch.ref, _byref(rq), _byref(rk),
+                                             _byref(rv), wq, wk, pos, _byref(_rows(q_out, qs, dev, "q_out")),
+                                             self._refs[1], s), "pnmix_kv4_append_qkv")
         return q_out
 
     def read(self, batch: KV4Batch, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
              stream=None):
         """The batch's rows as the cache holds them: (k, v) bf16 [n][Hkv][head_dim]."""
-        H, D, n, dev = self.cfg.n_kv_heads, self.cfg.head_dim, batch.n_tokens, self.device
-        with self._on(batch, stream) as s:
-            k_out = torch.empty((n, H, D), dtype=torch.bfloat16, device=dev) if k_out is None else k_out
-            v_out = torch.empty((n, H, D), dtype=torch.bfloat16, device=dev) if v_out is None else v_out
-            rk, rv = _rows(k_out, H, D, dev, "k_out", n), _rows(v_out, H, D, dev, "v_out", n)
-            _check(_lib.pnmix_kv4_read(self._refs[0], ctypes.byref(batch.c), self._refs[1], ctypes.byref(rk),
-                                       ctypes.byref(rv), s), "pnmix_kv4_read")
+        kv, dev = (batch.n_tokens, *self._kv), self.device
+        ctx, s = self._on(batch, stream)
+        with ctx:
+            k_out = torch.empty(kv, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
+            v_out = torch.empty_like(k_out) if v_out is None else v_out
+            _check(_lib.pnmix_kv4_read(self._refs[0], batch.ref, self._refs[1],
+                                       _byref(_rows(k_out, kv, dev, "k_out")),
+                                       _byref(_rows(v_out, kv, dev, "v_out")), s), "pnmix_kv4_read")
         return k_out, v_out
 
     def attend(self, batch: KV4Batch, q: torch.Tensor, out: torch.Tensor | None = None,
@@ -285,21 +279,19 @@ class KV4Cache:
         """Causal attention of q bf16 [n][Hq][head_dim] over the pages -> bf16, same shape.
         The workspace (kv4_workspace_bytes) is taken from torch's allocator for the call unless
         one is given."""
-        c, n, dev = self.cfg, batch.n_tokens, self.device
-        rq = _rows(q, c.n_q_heads, c.head_dim, dev, "q", n)
-        need = _lib.pnmix_kv4_workspace_bytes(self._refs[0], ctypes.byref(batch.c))
-        with self._on(batch, stream) as s:
-            if out is None:
-                out = torch.empty((n, c.n_q_heads, c.head_dim), dtype=q.dtype, device=dev)
-            ro = _rows(out, c.n_q_heads, c.head_dim, dev, "out", n)
+        qs, dev = (batch.n_tokens, *self._q), self.device
+        rq = _rows(q, qs, dev, "q")
+        ctx, s = self._on(batch, stream)
+        with ctx:
+            out = q.new_empty(qs) if out is None else out
             if workspace is None:
-                workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-            elif not workspace.is_cuda or workspace.device != dev or workspace.dtype != torch.uint8 \
-                    or not workspace.is_contiguous():
+                need = _lib.pnmix_kv4_workspace_bytes(self._refs[0], batch.ref)
+                workspace = self.buffer.new_empty(max(need, 256))
+            elif workspace.device != dev or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
                 raise TypeError(f"workspace must be contiguous uint8 on {dev}")
-            _check(_lib.pnmix_kv4_attention(self._refs[0], ctypes.byref(batch.c), ctypes.byref(rq), self._refs[1],
-                                            ctypes.byref(ro), workspace.data_ptr(), workspace.numel(), s),
-                   "pnmix_kv4_attention")
+            _check(_lib.pnmix_kv4_attention(self._refs[0], batch.ref, _byref(rq), self._refs[1],
+                                            _byref(_rows(out, qs, dev, "out")), workspace.data_ptr(),
+                                            workspace.numel(), s), "pnmix_kv4_attention")
         return out
 
     def pages(self) -> torch.Tensor:
@@ -326,4 +318,4 @@ def kv4_cache_bytes(cfg: KV4Config, n_pages: int) -> int:
 
 
 def kv4_workspace_bytes(cfg: KV4Config, batch: KV4Batch) -> int:
-    return int(_lib.pnmix_kv4_workspace_bytes(ctypes.byref(cfg), ctypes.byref(batch.c)))
+    return int(_lib.pnmix_kv4_workspace_bytes(_byref(cfg), batch.ref))
