@@ -22,7 +22,10 @@ namespace pnmix {
 namespace kv4 {
 
 struct UnitInfo {     // of the unit that begins in a CTA and ends in `last`; last < 0: there is none
-  int last, b, h, tile;
+  int last;
+  int start, h;             // the sequence's first row, KV head
+  int row_first, rows;      // of the unit
+  int pad[3];
 };
 
 struct Work {
@@ -219,7 +222,8 @@ __device__ __forceinline__ void for_each_piece(const Geo& g, const Batch& bt, in
     p.hi = static_cast<int>(max(xe - ustart - lead, 0ll));
     p.whole = first == last;
     p.slot = slot_of(blockIdx.x, first);
-    if (writer && x == ustart && !p.whole) wk.info[blockIdx.x] = {last, p.b, p.h, p.tile};
+    if (writer && x == ustart && !p.whole) 
+      wk.info[blockIdx.x] = {last, p.start, p.h, p.tile * RT, min(RT, p.T * g.G - p.tile * RT), {0, 0, 0}};
     if (!SOLO) __syncwarp();      // every lane has read the last piece and `next`
     if (scribe) {
       at->p = p;

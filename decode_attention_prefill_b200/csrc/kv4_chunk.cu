@@ -208,7 +208,7 @@ struct Smem {
   static constexpr int kHalfBytes = 4 * 20 * D;             // 4 blocks
   static constexpr int kMl = 0;                             // after the ring: [128][2], stream 1's m, l
   static constexpr int kBars = kMl + 128 * 8;
-  static constexpr int kJobs = kBars + 320;                 // two pieces of work
+  static constexpr int kJobs = kBars + 384;                 // two pieces of work
   static constexpr int kSlots = kJobs + 96;                 // the partition's place in its work
   static constexpr int kEnd = kSlots + 64;
   __host__ __device__ static constexpr int ring(bool dual) { return kQ + (dual ? 2 : 1) * kTileBytes; }
@@ -260,7 +260,7 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
   uint64_t* s_full = bars + 12;      // [2] logits of the stream are in TMEM
   uint64_t* p_full = bars + 14;      // [2] its weights are (4 warps)
   uint64_t* o_done = bars + 16;      // [2] its value products of this piece are done
-  uint64_t* q_full = bars + 18;      // query tiles written (8 warps)
+  uint64_t* q_full = bars + 38;      // [2] the stream's query tile is written (4 warps)
   uint64_t* job_full = bars + 19;    // [2]
   uint64_t* job_empty = bars + 21;   // [2] every role is done with it (16 warps and two more)
   uint64_t* drained = bars + 23;
@@ -279,11 +279,11 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
       mbar_init(v_empty + i, 1);
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
+      mbar_init(q_full + i, 4);
       mbar_init(o_done + i, 1);
       mbar_init(job_full + i, 1);
       mbar_init(job_empty + i, 18);
     }
-    mbar_init(q_full, 8);
     mbar_init(drained, 1);
     *fail = 0;
     fence_mbar_init();
@@ -334,21 +334,22 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
     float* ml = reinterpret_cast<float*>(rest + S::kMl) + 2 * row;
     uint8_t* qa = smem + S::kQ + (dual ? stream * S::kTileBytes : 0);
     uint32_t ns = 0, no = 0;   // logit tiles taken; pieces whose value products were waited for
-    // whether any thread of the two streams says so (they go on or stop alike)
+    // whether any thread says so, of the stream (two-tile form) or of both
     auto either = [&](bool x) -> bool {
       uint32_t any;
       asm volatile(
-          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
           : "=r"(any)
-          : "r"(static_cast<uint32_t>(x))
+          : "r"(static_cast<uint32_t>(x)), "r"(dual ? 2 + stream : 1), "r"(dual ? 128 : 256)
           : "memory");
       return any != 0;
     };
     bool ok = true;
     for (uint32_t job = 0;; ++job) {
       ok = ok && wait(job_full + (job & 1u), job >> 1, kCommitLimit);
-      // every thread is done with the last piece (its query tile, its O, ml)
-      if (either(!ok || *fail)) break;
+      // In the one-tile form both streams are done with the last piece here (its query tile, O and
+      // ml) and go on or stop alike; else a stream's warps are, with its query tile.
+      if (either(!ok)) break;
       const Job& jb = jobs[job & 1u];
       const int nt = jb.n;
       if (nt < 0) break;
@@ -419,7 +420,7 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
       }
       proxy_fence();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      if (lane == 0) mbar_arrive(q_full + stream);
       if (!dual) {          // stream 1 has the same rows
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (stream == 1) fac = ml[0];
@@ -744,8 +745,8 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
       };
       for_each_job([&](const Job& jb) -> bool {
         const int n = jb.n, ahead = dual ? 1 : 2;
-        if (!wait(q_full, nq++, kCommitLimit)) return false;
-        tc_fence_after();
+        // (in the one-tile form the second stream reads the first one's tile)
+        if (!wait(q_full, nq, kCommitLimit)) return false;
         // the next key tile, once written
         auto key_tile = [&]() -> bool {
           if (!wait(k_full + (nk & 1u), nk >> 1, kCommitLimit)) return false;
@@ -755,10 +756,15 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
         for (int i = 0; i < ahead && i < n; ++i) {
           if (!key_tile()) return false;
           logits(dual ? 0 : i, nk & 1u);
-          if (dual) logits(1, nk & 1u);
+          if (dual) {
+            if (!wait(q_full + 1, nq, kCommitLimit)) return false;
+            logits(1, nk & 1u);
+          }
           tc_commit(k_empty + (nk & 1u));
           ++nk;
         }
+        if (dual && n == 0 && !wait(q_full + 1, nq, kCommitLimit)) return false;     // no phase is skipped
+        ++nq;
         for (int i = 0; i < n; ++i) {
           for (int x = 0; x < (dual ? 2 : 1); ++x) {
             const int stream = dual ? x : i & 1;

@@ -505,40 +505,56 @@ merge_kernel(const __grid_constant__ AttnArgs a, int RT) {
   const int first = blockIdx.x;
   const UnitInfo f = a.wk.info[first];
   if (f.last < 0) return;
-  int start, T;
-  seq_rows(a.bt, f.b, start, T);
-  const int nrows = min(RT, T * a.g.G - f.tile * RT), n = f.last - first + 1;
+  const int n = f.last - first + 1;
   const int v0 = blockIdx.y * kRows, r = threadIdx.x & (kRows - 1), c0 = threadIdx.x / kRows, v = v0 + r;
-  if (v0 >= nrows) return;
-  auto part = [&](int k) { return part_of<D>(a.wk.part, slot_of(first + k, first), RT); };
+  if (v0 >= f.rows) return;
+  // kAhead partials at a time, all of their loads first: few partials are one round trip
+  constexpr int kAhead = 8, kC = C4 / kLanes;
   float m = -1e30f, l = 0.f;
-  float4 o[C4 / kLanes];
+  float4 o[kC];
 #pragma unroll
-  for (int i = 0; i < C4 / kLanes; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (v < nrows) {
-    for (int k = 0; k < n; ++k) {
-      const float2 x = reinterpret_cast<const float2*>(part(k))[v];
-      if (x.y != 0.f) m = fmaxf(m, x.x);      // a partial that saw nothing has l = 0
-    }
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float* p = part(k);
-      const float2 x = reinterpret_cast<const float2*>(p)[v];
-      const float w = x.y == 0.f ? 0.f : ex2(x.x - m);
-      l = fmaf(x.y, w, l);
+  for (int i = 0; i < kC; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (v < f.rows) {
+    for (int k0 = 0; k0 < n; k0 += kAhead) {
+      float2 x[kAhead];
+      float4 t[kAhead][kC];
 #pragma unroll
-      for (int i = 0; i < C4 / kLanes; ++i) {
-        const float4 t = reinterpret_cast<const float4*>(p + 2 * RT)[(c0 + i * kLanes) * RT + v];
-        o[i].x = fmaf(t.x, w, o[i].x);
-        o[i].y = fmaf(t.y, w, o[i].y);
-        o[i].z = fmaf(t.z, w, o[i].z);
-        o[i].w = fmaf(t.w, w, o[i].w);
+      for (int k = 0; k < kAhead; ++k) {
+        x[k] = make_float2(-1e30f, 0.f);
+        if (k0 + k < n) {
+          const float* p = part_of<D>(a.wk.part, slot_of(first + k0 + k, first), RT);
+          x[k] = reinterpret_cast<const float2*>(p)[v];
+#pragma unroll
+          for (int i = 0; i < kC; ++i) t[k][i] = reinterpret_cast<const float4*>(p + 2 * RT)[(c0 + i * kLanes) * RT + v];
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (x[k].y != 0.f) top = fmaxf(top, x[k].x);      // a partial that saw nothing has l = 0
+      const float old = ex2(m - top);
+      m = top;
+      l *= old;
+#pragma unroll
+      for (int i = 0; i < kC; ++i) o[i] = make_float4(o[i].x * old, o[i].y * old, o[i].z * old, o[i].w * old);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (x[k].y == 0.f) continue;
+        const float w = ex2(x[k].x - m);
+        l = fmaf(x[k].y, w, l);
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          o[i].x = fmaf(t[k][i].x, w, o[i].x);
+          o[i].y = fmaf(t[k][i].y, w, o[i].y);
+          o[i].z = fmaf(t[k][i].z, w, o[i].z);
+          o[i].w = fmaf(t[k][i].w, w, o[i].w);
+        }
       }
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int i = 0; i < C4 / kLanes; ++i) {
+  for (int i = 0; i < kC; ++i) {
     const __nv_bfloat162 lo = __floats2bfloat162_rn(o[i].x * inv, o[i].y * inv);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(o[i].z * inv, o[i].w * inv);
     float2 pk;
@@ -549,9 +565,9 @@ merge_kernel(const __grid_constant__ AttnArgs a, int RT) {
   __syncthreads();
   for (int i = threadIdx.x; i < kRows * C4; i += kThreads) {
     const int rr = i / C4, c = i - rr * C4;
-    if (v0 + rr >= nrows) break;
-    const int row = f.tile * RT + v0 + rr, j = row / a.g.G, hg = row - j * a.g.G;
-    uint16_t* dst = a.out + static_cast<long long>(start + j) * a.out_ts + (f.h * a.g.G + hg) * a.out_hs;
+    if (v0 + rr >= f.rows) break;
+    const int row = f.row_first + v0 + rr, j = row / a.g.G, hg = row - j * a.g.G;
+    uint16_t* dst = a.out + static_cast<long long>(f.start + j) * a.out_ts + (f.h * a.g.G + hg) * a.out_hs;
     reinterpret_cast<float2*>(dst)[c] = out_tile[rr][c];
   }
 }
@@ -583,11 +599,19 @@ constexpr int kMaxCtas = 1024;
 
 }  // namespace
 
-// Query rows of a unit.  Up to 8 or 16 rows of a sequence and KV head take the kernel above,
-// more the tcgen05 one.
+// Query rows of a unit: 8 or 16 in the kernel above, which passes over the pages once per unit,
+// 128 or 256 in the tcgen05 one, whose time hardly depends on the rows up to 128.  By the rows
+// that a sequence has on the average for a KV head (rows = G * tokens), measured:
+//   head_dim 128, 16 x 32K x 8 heads:  16 rows 283 us, 24 rows 416 against 398 us, 48 rows 618
+//     against 394 us; 8 x 8K x 8 heads:  24 rows 70 against 72 us, 48 rows 98 against 73 us
+//   head_dim 64, 8 x 8K x 8 heads:  20 rows 48 against 68 us, 48 rows 66 against 68 us, 64 rows
+//     82 against 66 us
 static int tile_rows(const Geo& g, const Batch& bt) {
-  const int rows = g.G * bt.max_q;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
+  const int most = g.G * bt.max_q;
+  const double mean = static_cast<double>(g.G) * bt.n_tokens / bt.B;
+  if (most <= 8) return 8;
+  if (most <= 16 || (most <= 128 && mean <= (g.D == 128 ? 24 : 48))) return 16;
+  return most <= 128 ? 128 : 256;
 }
 
 static int most_ctas(int rt) { return rt > 16 ? kMaxChunkCtas : kMaxCtas; }
@@ -638,7 +662,7 @@ cudaError_t launch_attention(const Geo& g, const Batch& bt, const pnmix_rows& q,
   a.out = out.data;
   a.out_ts = out.token_stride;
   a.out_hs = out.head_stride;
-  a.grain = {384, 128};
+  a.grain = {384, 256};
   a.wk.info = static_cast<UnitInfo*>(ws);
   a.wk.part = reinterpret_cast<float*>(static_cast<char*>(ws) + info_bytes(rt));
   int ctas = 0;

@@ -22,8 +22,11 @@ namespace pnmix {
 namespace kv4 {
 namespace {
 
-constexpr int kIoThreads = 128;
-constexpr int kRowsPass = kIoThreads / 4;   // rows a CTA works on at once
+// Threads of a CTA; a row takes four.  Measured at the large cases (128 / 256 threads): norm and
+// rotation 59 / 66 us, write and read back 54 / 57 us with 128 threads in the read-back's kernel
+// too, which alone takes 66 / 61 us.
+constexpr int kInThreads = 128, kOutThreads = 256;
+constexpr int kInRows = kInThreads / 4, kOutRows = kOutThreads / 4;   // rows a CTA works on at once
 constexpr int kMaxTok = 16;                 // tokens per CTA at most
 
 // Sequence of packed row `row`: the last b with q_start[b] <= row, or -1 for a row outside
@@ -87,16 +90,50 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Minimum / maximum that return NaN if either is one.
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float d;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+// Minimum / maximum of bf16 pairs that return NaN where either is one.
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+
+// Codes of eight bf16 values for scale s16 / zero z16 (packed in sz) and inv = rcp_rn(s), 0 if
+// s is 0.  The contract's code is rint(fl(fl(x - z) / s)) clamped to [0, 15].  Here
+//     u = sat(x * (inv / 15) - z * (inv / 15)),  code = rint(15 u),
+// six instructions a code: the saturation clamps, the rounding is an addition of 1.5 * 2^23,
+// and the sums' low bits are put together by multiply-adds.  15 u is off the quotient by less
+// than 2^-15 while |z / s| <= 256 (the rounded z * inv / 15 counts 2^-24 |z / s|, the other
+// roundings together less than 2^-17), so the code can differ only where 15 u is that near to
+// a half-integer; there, and for larger |z / s|, the codes are worked out by the contract.
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], uint32_t sz, float inv) {
+  constexpr float kMagic = 12582912.f;
+  const float z = __half2float(__ushort_as_half(static_cast<uint16_t>(sz >> 16)));
+  const float step = inv * (1.f / 15.f), base = -z * step;
+  uint32_t word = 0u - 0x4B400000u * 0x11111111u;
+  float far = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float u = __saturatef(fmaf(x[i], step, base));
+    const float y = fmaf(u, 15.f, kMagic);
+    far = fmaxf(far, fabsf(fmaf(u, 15.f, kMagic - y)));
+    word += __float_as_uint(y) << (4 * i);
+  }
+  if (far < 0.5f - 0x1p-14f && fabsf(z * inv) <= 256.f) return word;
+  const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(sz & 0xFFFFu)));
+  word = 0u;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    float xi = x[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) xi = i == k ? x[k] : xi;
+    if (s != 0.f) word |= quant_code_rcp(xi, z, s, inv, 15) << (4 * i);
+  }
+  return word;
 }
 
 // n words (2 or 4) as one access.
@@ -164,7 +201,7 @@ __host__ __device__ __forceinline__ int turn_stride(int half) { return 2 * half 
 // ROPE: q and k rows are normed and rotated.  QUANT: k and v rows go to the cache (otherwise
 // k rows are stored like q's).
 template <int D, bool ROPE, bool QUANT, int PAIRS>
-__global__ void __launch_bounds__(kIoThreads)
+__global__ void __launch_bounds__(kInThreads)
 rows_in_kernel(const __grid_constant__ IoArgs a) {
   constexpr int NG = D / 32;
   extern __shared__ __align__(16) float shared[];   // [token][cos, sin], then [warp][8 rows][D + 4]
@@ -205,7 +242,7 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
   load(mine, next);
 
   if (QUANT) {
-    for (int i = warp; i < ntok; i += kIoThreads / 32) {
+    for (int i = warp; i < ntok; i += kInThreads / 32) {
       long long off;
       int tok;
       row_place(a.g, a.bt, tok0 + i, lane, off, tok);
@@ -216,7 +253,7 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
     }
   }
   if (ROPE) {
-    for (int i = tid; i < half << a.tok_shift; i += kIoThreads) {
+    for (int i = tid; i < half << a.tok_shift; i += kInThreads) {
       const int t = i / half, p = i - t * half;
       float s = 0.f, c = 1.f;
       if (tok0 + t < a.n_tokens) {
@@ -232,17 +269,20 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
       shared[t * turn_stride(half) + half + p] = s;
     }
   }
-  if (ROPE || QUANT) __syncthreads();
+  if (ROPE) __syncthreads();      // without a rotation the places are first needed behind the codes
 
-  for (int rho = mine; rho - mine < total; rho += kRowsPass) {
-    float x[8 * NG];
+  for (int rho = mine; rho - mine < total; rho += kInRows) {
+    uint4 raw[NG];
 #pragma unroll
-    for (int k = 0; k < NG; ++k) unpack8(next[k], x + 8 * k);
-    if (rho - mine + kRowsPass < total) load(rho + kRowsPass, next);
+    for (int k = 0; k < NG; ++k) raw[k] = next[k];
+    if (rho - mine + kInRows < total) load(rho + kInRows, next);
     int t, head;
     const int kind = find(rho, t, head);
     if (ROPE && __any_sync(0xffffffffu, kind == 0 || kind == 1)) {
       // value rows in the same warp go through it too, as rows without a rotation
+      float x[8 * NG];
+#pragma unroll
+      for (int k = 0; k < NG; ++k) unpack8(raw[k], x + 8 * k);
       const bool turns = kind == 0 || kind == 1;
       const uint16_t* wt = kind == 0 ? a.qw : a.kw;
       float ss = 0.f;
@@ -336,26 +376,26 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
       }
       if (QUANT) {   // keys enter the cache as the bf16 row a separate call would write
 #pragma unroll
-        for (int k = 0; k < NG; ++k) unpack8(b[k], x + 8 * k);
+        for (int k = 0; k < NG; ++k) raw[k] = b[k];
       }
     }
     if constexpr (QUANT) {
-      if (!__any_sync(0xffffffffu, kind > 0)) continue;
+      if (ROPE && !__any_sync(0xffffffffu, kind > 0)) continue;
       float mn[NG], mx[NG];
       auto range = [&]() {
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-          mn[k] = mx[k] = x[8 * k];
-#pragma unroll
-          for (int i = 1; i < 8; ++i) {
-            mn[k] = min_nan(mn[k], x[8 * k + i]);
-            mx[k] = max_nan(mx[k], x[8 * k + i]);
-          }
+          uint32_t lo = min2_nan(min2_nan(raw[k].x, raw[k].y), min2_nan(raw[k].z, raw[k].w));
+          uint32_t hi = max2_nan(max2_nan(raw[k].x, raw[k].y), max2_nan(raw[k].z, raw[k].w));
 #pragma unroll
           for (int o = 1; o < 4; o <<= 1) {
-            mn[k] = min_nan(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], o));
-            mx[k] = max_nan(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+            lo = min2_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = max2_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
           }
+          lo = min2_nan(lo, lo >> 16);      // the pair's, in the low half
+          hi = max2_nan(hi, hi >> 16);
+          mn[k] = __uint_as_float(lo << 16);
+          mx[k] = __uint_as_float(hi << 16);
         }
       };
       range();
@@ -364,21 +404,36 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
       for (int k = 0; k < NG; ++k) odd |= !(mn[k] >= -kLimit && mx[k] <= kLimit);
       if (__any_sync(0xffffffffu, odd)) {   // a NaN or a number past the limit: taken inside
 #pragma unroll
-        for (int i = 0; i < 8 * NG; ++i) x[i] = x[i] == x[i] ? fminf(fmaxf(x[i], -kLimit), kLimit) : 0.f;
+        for (int k = 0; k < NG; ++k) {
+          float y[8];
+          unpack8(raw[k], y);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = y[i] == y[i] ? fminf(fmaxf(y[i], -kLimit), kLimit) : 0.f;
+          raw[k] = pack8(y);                // exact: the limit is a bf16
+        }
         range();
       }
+      // lane w works out the scale, zero and reciprocal of group w (of w % 2 with two groups)
+      const int own = w & (NG - 1);
+      float lo = mn[0], hi = mx[0];
+#pragma unroll
+      for (int k = 1; k < NG; ++k) {
+        lo = own == k ? mn[k] : lo;
+        hi = own == k ? mx[k] : hi;
+      }
+      const QParams qp = quant_params(lo, hi, 4);
+      const uint32_t sz_own = static_cast<uint32_t>(qp.s16) | (static_cast<uint32_t>(qp.z16) << 16);
+      const float inv_own = qp.s != 0.f ? __frcp_rn(qp.s) : 0.f;
       uint32_t code[NG], sz[NG];
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
-        const QParams qp = quant_params(mn[k], mx[k], 4);
-        code[k] = 0u;
-        if (qp.s != 0.f) {
-          const float inv = __frcp_rn(qp.s);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) code[k] |= quant_code_rcp(x[8 * k + i], qp.z, qp.s, inv, 15) << (4 * i);
-        }
-        sz[k] = static_cast<uint32_t>(qp.s16) | (static_cast<uint32_t>(qp.z16) << 16);
+        sz[k] = __shfl_sync(0xffffffffu, sz_own, k, 4);
+        const float inv = __shfl_sync(0xffffffffu, inv_own, k, 4);
+        float y[8];
+        unpack8(raw[k], y);
+        code[k] = codes_of(y, sz[k], inv);
       }
+      if (!ROPE && rho == mine) __syncthreads();      // every thread's first row
       if (kind > 0 && place[t] >= 0) {
         const int tok = place_tok[t];
         uint8_t* blk = a.g.pages + place[t] + static_cast<size_t>(head) * ((1 << (a.g.page_shift - 4)) * block_bytes(D)) +
@@ -408,7 +463,7 @@ struct OutArgs {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kIoThreads)
+__global__ void __launch_bounds__(kOutThreads)
 rows_out_kernel(const __grid_constant__ OutArgs a) {
   constexpr int NG = D / 32, kAhead = 2;
   __shared__ long long place[kMaxTok];
@@ -417,7 +472,7 @@ rows_out_kernel(const __grid_constant__ OutArgs a) {
   const int ntok = 1 << a.tok_shift, tok0 = blockIdx.x << a.tok_shift;
   const int row0 = blockIdx.y * a.rows_y, rows = min(a.rows_y, 2 * a.g.Hkv - row0);
   const int total = rows << a.tok_shift;
-  for (int i = warp; i < ntok; i += kIoThreads / 32) {
+  for (int i = warp; i < ntok; i += kOutThreads / 32) {
     long long off;
     int tok;
     row_place(a.g, a.bt, tok0 + i, lane, off, tok);
@@ -428,11 +483,11 @@ rows_out_kernel(const __grid_constant__ OutArgs a) {
   }
   __syncthreads();
   const size_t head_bytes = static_cast<size_t>(1 << (a.g.page_shift - 4)) * block_bytes(D);
-  for (int rho0 = tid >> 2; rho0 < total; rho0 += kAhead * kRowsPass) {
+  for (int rho0 = tid >> 2; rho0 < total; rho0 += kAhead * kOutRows) {
     uint32_t code[kAhead][NG], sz[kAhead][NG];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int rho = rho0 + u * kRowsPass, t = rho & (ntok - 1), r = row0 + (rho >> a.tok_shift);
+      const int rho = rho0 + u * kOutRows, t = rho & (ntok - 1), r = row0 + (rho >> a.tok_shift);
 #pragma unroll
       for (int k = 0; k < NG; ++k) code[u][k] = sz[u][k] = 0u;
       if (rho < total && place[t] >= 0) {
@@ -445,7 +500,7 @@ rows_out_kernel(const __grid_constant__ OutArgs a) {
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int rho = rho0 + u * kRowsPass, t = rho & (ntok - 1), r = row0 + (rho >> a.tok_shift);
+      const int rho = rho0 + u * kOutRows, t = rho & (ntok - 1), r = row0 + (rho >> a.tok_shift);
       if (rho >= total || place[t] == -2) continue;
       if (r & 1) {
         uint32_t c[NG];
@@ -476,10 +531,12 @@ rows_out_kernel(const __grid_constant__ OutArgs a) {
   }
 }
 
-// Tokens per CTA: eight make a warp's rows neighbours in the cache; fewer while the grid would
-// not fill the GPU.
-int token_shift(int n_tokens) {
-  int s = 3;
+// Tokens per CTA at most (log2; neighbours in the cache are written by one warp), fewer while
+// the grid would not fill the GPU.  Measured at 16384 tokens with 1, 2, 4 and 8 tokens: norm and
+// rotation of 40 heads -, 59, 61 and 72 us; the write of 16 rows a token (and its read-back) -,
+// 55, 54 and 55 us.
+int token_shift(int n_tokens, int most) {
+  int s = most;
   while (s > 0 && (n_tokens >> s) < 4 * 148) --s;
   return s;
 }
@@ -489,14 +546,14 @@ cudaError_t launch_pairs(const IoArgs& a, cudaStream_t s) {
   const int ctas = (a.n_tokens + (1 << a.tok_shift) - 1) >> a.tok_shift;
   size_t floats = 0;
   if (ROPE) floats += static_cast<size_t>(turn_stride(a.rope.rot_dim >> 1)) << a.tok_shift;
-  if (ROPE && PAIRS == kAnywhere) floats += kIoThreads / 4 * (D + 4);
-  rows_in_kernel<D, ROPE, QUANT, PAIRS><<<ctas, kIoThreads, floats * sizeof(float), s>>>(a);
+  if (ROPE && PAIRS == kAnywhere) floats += kInRows * (D + 4);
+  rows_in_kernel<D, ROPE, QUANT, PAIRS><<<ctas, kInThreads, floats * sizeof(float), s>>>(a);
   return cudaGetLastError();
 }
 
 template <int D, bool ROPE, bool QUANT>
 cudaError_t launch_in(IoArgs& a, cudaStream_t s) {
-  a.tok_shift = token_shift(a.n_tokens);
+  a.tok_shift = token_shift(a.n_tokens, ROPE ? 1 : 2);
   if constexpr (!ROPE) {
     return launch_pairs<D, ROPE, QUANT, kHalves>(a, s);
   } else {
@@ -581,13 +638,13 @@ cudaError_t launch_read(const Geo& g, const Batch& bt, const pnmix_rows& k, cons
   a.tok_shift = 4;
   while (a.tok_shift > 0 && (bt.n_tokens >> a.tok_shift) < 148) --a.tok_shift;
   const int x = (bt.n_tokens + (1 << a.tok_shift) - 1) >> a.tok_shift, rows = 2 * g.Hkv;
-  a.rows_y = max(1, 2 * kRowsPass >> a.tok_shift);
+  a.rows_y = max(1, 2 * kOutRows >> a.tok_shift);
   while (a.rows_y < rows && static_cast<long long>(x) * ((rows + a.rows_y - 1) / a.rows_y) > 148 * 16) a.rows_y *= 2;
   const dim3 grid(x, (rows + a.rows_y - 1) / a.rows_y);
   if (g.D == 64)
-    rows_out_kernel<64><<<grid, kIoThreads, 0, s>>>(a);
+    rows_out_kernel<64><<<grid, kOutThreads, 0, s>>>(a);
   else
-    rows_out_kernel<128><<<grid, kIoThreads, 0, s>>>(a);
+    rows_out_kernel<128><<<grid, kOutThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
