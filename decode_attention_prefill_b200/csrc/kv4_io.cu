@@ -102,36 +102,34 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Codes of eight bf16 values for scale s16 / zero z16 (packed in sz) and inv = rcp_rn(s), 0 if
-// s is 0.  The contract's code is rint(fl(fl(x - z) / s)) clamped to [0, 15].  Here
-//     u = sat(x * (inv / 15) - z * (inv / 15)),  code = rint(15 u),
-// six instructions a code: the saturation clamps, the rounding is an addition of 1.5 * 2^23,
-// and the sums' low bits are put together by multiply-adds.  15 u is off the quotient by less
-// than 2^-15 while |z / s| <= 256 (the rounded z * inv / 15 counts 2^-24 |z / s|, the other
-// roundings together less than 2^-17), so the code can differ only where 15 u is that near to
-// a half-integer; there, and for larger |z / s|, the codes are worked out by the contract.
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], uint32_t sz, float inv) {
+// The contract's code is rint(fl(fl(x - z) / s)) clamped to [0, 15].  The correctly rounded
+// quotient comes from the correctly rounded reciprocal inv = fl(1 / s) without a division
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990): with d = fl(x - z) and q = fl(d inv), fl(q + fl(d - q s) inv) = fl(d / s), the residual
+// being exact.  The rounding to a whole number is an addition of 1.5 * 2^23.  (Deciding by q
+// alone and dividing only near half-integers took longer: bf16 differences over an fp16 scale
+// are exact half-integers once in 1500 values, so half of the warps had one to divide.)
+__device__ __forceinline__ float code_sum(float x, float z, float s, float inv) {
   constexpr float kMagic = 12582912.f;
-  const float z = __half2float(__ushort_as_half(static_cast<uint16_t>(sz >> 16)));
-  const float step = inv * (1.f / 15.f), base = -z * step;
-  uint32_t word = 0u - 0x4B400000u * 0x11111111u;
-  float far = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float u = __saturatef(fmaf(x[i], step, base));
-    const float y = fmaf(u, 15.f, kMagic);
-    far = fmaxf(far, fabsf(fmaf(u, 15.f, kMagic - y)));
-    word += __float_as_uint(y) << (4 * i);
-  }
-  if (far < 0.5f - 0x1p-14f && fabsf(z * inv) <= 256.f) return word;
+  const float d = __fsub_rn(x, z), q = __fmul_rn(d, inv);
+  return __fadd_rn(__fmaf_rn(__fmaf_rn(-q, s, d), inv, q), kMagic);      // the code in its low bits
+}
+
+// Codes of eight values; `plain`: none needs the clamp.
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], uint32_t sz, float inv, bool plain) {
   const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(sz & 0xFFFFu)));
-  word = 0u;
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    float xi = x[0];
+  const float z = __half2float(__ushort_as_half(static_cast<uint16_t>(sz >> 16)));
+  if (plain) {
+    uint32_t word = 0u - 0x4B400000u * 0x11111111u;
 #pragma unroll
-    for (int k = 1; k < 8; ++k) xi = i == k ? x[k] : xi;
-    if (s != 0.f) word |= quant_code_rcp(xi, z, s, inv, 15) << (4 * i);
+    for (int i = 0; i < 8; ++i) word += __float_as_uint(code_sum(x[i], z, s, inv)) << (4 * i);
+    return word;
+  }
+  uint32_t word = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = __float_as_int(code_sum(x[i], z, s, inv)) - 0x4B400000;
+    word |= static_cast<uint32_t>(min(max(c, 0), 15)) << (4 * i);
   }
   return word;
 }
@@ -423,7 +421,12 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
       }
       const QParams qp = quant_params(lo, hi, 4);
       const uint32_t sz_own = static_cast<uint32_t>(qp.s16) | (static_cast<uint32_t>(qp.z16) << 16);
-      const float inv_own = qp.s != 0.f ? __frcp_rn(qp.s) : 0.f;
+      const float inv_own = qp.s != 0.f ? __frcp_rn(qp.s) : 0.f;      // 0 makes every code 0
+      // the codes of a group lie between those of its ends, which the rounding of s and z can push
+      // out of [0, 15]
+      const bool in_range = __float_as_uint(code_sum(lo, qp.z, qp.s, inv_own)) >= 0x4B400000u &&
+                            __float_as_uint(code_sum(hi, qp.z, qp.s, inv_own)) <= 0x4B40000Fu;
+      const bool plain = __all_sync(0xffffffffu, in_range);
       uint32_t code[NG], sz[NG];
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
@@ -431,7 +434,7 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
         const float inv = __shfl_sync(0xffffffffu, inv_own, k, 4);
         float y[8];
         unpack8(raw[k], y);
-        code[k] = codes_of(y, sz[k], inv);
+        code[k] = codes_of(y, sz[k], inv, plain);
       }
       if (!ROPE && rho == mine) __syncthreads();      // every thread's first row
       if (kind > 0 && place[t] >= 0) {
