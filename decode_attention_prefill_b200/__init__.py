@@ -55,7 +55,7 @@ EXPORTED = [
     "pnmix_decode_attention_two", "pnmix_append_decode",
     "pnmix_norm_rope", "pnmix_kv4_cache_bytes", "pnmix_kv4_cache_init", "pnmix_kv4_cache_reset",
     "pnmix_kv4_append", "pnmix_kv4_append_qkv", "pnmix_kv4_read", "pnmix_kv4_workspace_bytes",
-    "pnmix_kv4_attention", "pnmix_kv4_read_error",
+    "pnmix_kv4_attention", "pnmix_debug_kv4_stall", "pnmix_kv4_read_error",
 ]
 
 
@@ -384,8 +384,38 @@ class PNMixCache:
         pnmix_quantize_keys(self.cfg, k, L, self, stream)
         pnmix_quantize_values(self.cfg, v, L, self, stream)
 
+    def prefill_projected(self, rope: "Rope", q, k, v, positions, q_weight=None, k_weight=None, stream=None):
+        """prefill() from a model's projections: q bf16 [B][L][Hq][128], k, v bf16 [B][L][Hkv][128]
+        before norm and rotation, positions int32 [B][n_axes][L] ([B][L] with one axis).  Every
+        head is normed (where a weight is given) and rotated by norm_rope, straight into the
+        head-major tensors that prefill takes.  Returns the rotated keys, [B][Hkv][L][128]."""
+        from .kv4 import _on
+        B, L, Hq, D = q.shape
+        W = min(L, self.cfg.saliency_window)
+        with _on(q.device, stream)[0]:
+            q_win = q.new_empty(B, Hq, W, D)
+            k_rot = k.new_empty(B, k.shape[2], L, D)
+            pos = positions.view(B, -1, L)
+            for b in range(B):
+                norm_rope(rope, q[b, L - W:], None, pos[b, :, L - W:].contiguous(), q_weight,
+                          q_out=q_win[b].transpose(0, 1))
+                norm_rope(rope, None, k[b], pos[b].contiguous(), None, k_weight, k_out=k_rot[b].transpose(0, 1))
+            self.prefill(q_win, k_rot, v.transpose(1, 2).contiguous(), L)
+        return k_rot
+
     def append(self, k_new, v_new, stream=None):
         pnmix_append(self.cfg, k_new, v_new, self, stream)
+
+    def step_projected(self, rope: "Rope", q, k, v, positions, q_weight=None, k_weight=None, out=None, stream=None):
+        """One decode step from a model's projections: q bf16 [B][Hq][128], k, v bf16 [B][Hkv][128]
+        before norm and rotation (views of one projection, say), positions int32 [n_axes][B] ([B]
+        with one axis).  norm_rope, then pnmix_append_decode: fp32 [B][Hq][128]."""
+        from .kv4 import _on
+        with _on(q.device, stream)[0]:
+            q, k = norm_rope(rope, q, k, positions, q_weight, k_weight)
+            out = torch.empty(q.shape, dtype=torch.float32, device=q.device) if out is None else out
+            pnmix_append_decode(self.cfg, k, v.contiguous(), q, self, out)
+        return out
 
     def shrunk(self, stream=None, max_queries: int = 1) -> "PNMixCache":
         """A new cache holding this one with its salient keys shrunk to key_bits_lo bits."""

@@ -31,6 +31,7 @@ pnmix_status check_config(const pnmix_kv4_config* c, Geo* g) {
   g->page_shift = c->page_tokens == 16 ? 4 : c->page_tokens == 32 ? 5 : c->page_tokens == 64 ? 6 : 7;
   g->scale = c->softmax_scale > 0.f ? c->softmax_scale : 1.0f / sqrtf(static_cast<float>(g->D));
   g->wait_limit = kWaitLimit;
+  g->skip_seq = -1;
   return PNMIX_OK;
 }
 
@@ -227,12 +228,9 @@ size_t pnmix_kv4_workspace_bytes(const pnmix_kv4_config* cfg, const pnmix_kv4_ba
   return attention_workspace_bytes(g, bt);
 }
 
-pnmix_status pnmix_kv4_attention(const pnmix_kv4_config* cfg, const pnmix_kv4_batch* batch, const pnmix_rows* q,
-                                 const pnmix_kv4_cache* cache, const pnmix_rows* out, void* workspace,
-                                 size_t workspace_bytes, void* stream) {
-  Geo g;
+static pnmix_status attention(Geo g, const pnmix_kv4_batch* batch, const pnmix_rows* q, const pnmix_kv4_cache* cache,
+                              const pnmix_rows* out, void* workspace, size_t workspace_bytes, void* stream) {
   Batch bt;
-  PNMIX_TRY(check_config(cfg, &g));
   PNMIX_TRY(check_cache(cache, &g));
   PNMIX_TRY(check_batch(batch, g, &bt));
   if (bt.n_tokens == 0) return PNMIX_OK;
@@ -242,6 +240,25 @@ pnmix_status pnmix_kv4_attention(const pnmix_kv4_config* cfg, const pnmix_kv4_ba
   if (!aligned(workspace, 256)) return PNMIX_ERR_ALIGNMENT;
   if (workspace_bytes < attention_workspace_bytes(g, bt)) return PNMIX_ERR_CAPACITY;
   return cuda_status(launch_attention(g, bt, *q, *out, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+pnmix_status pnmix_kv4_attention(const pnmix_kv4_config* cfg, const pnmix_kv4_batch* batch, const pnmix_rows* q,
+                                 const pnmix_kv4_cache* cache, const pnmix_rows* out, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  Geo g;
+  PNMIX_TRY(check_config(cfg, &g));
+  return attention(g, batch, q, cache, out, workspace, workspace_bytes, stream);
+}
+
+pnmix_status pnmix_debug_kv4_stall(const pnmix_kv4_config* cfg, const pnmix_kv4_batch* batch, const pnmix_rows* q,
+                                   const pnmix_kv4_cache* cache, const pnmix_rows* out, void* workspace,
+                                   size_t workspace_bytes, int skip_seq, uint32_t wait_rounds, void* stream) {
+  Geo g;
+  PNMIX_TRY(check_config(cfg, &g));
+  if (!batch || skip_seq < 0 || skip_seq >= batch->batch || wait_rounds < 1) return PNMIX_ERR_INVALID_ARG;
+  g.skip_seq = skip_seq;
+  g.wait_limit = wait_rounds;
+  return attention(g, batch, q, cache, out, workspace, workspace_bytes, stream);
 }
 
 pnmix_status pnmix_kv4_read_error(const pnmix_kv4_cache* cache, int clear, uint32_t* host_error) {

@@ -19,7 +19,8 @@ struct Geo {
   float scale;
   uint8_t* pages;
   uint32_t* error;
-  uint32_t wait_limit;    // try_wait rounds before a staging wait gives up
+  uint32_t wait_limit;    // try_wait rounds before a wait for staged pages gives up
+  int skip_seq;           // test hook: the sequence whose pages are never staged (-1: none)
 };
 
 // A validated batch.

@@ -303,8 +303,8 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
   const uint32_t tmem = *tmem_holder;
 
   // Bounded wait for phase `n` (counted from 0) of a barrier; false once anything in the CTA
-  // gave up.
-  auto wait = [&](uint64_t* bar, uint32_t n, uint32_t limit) -> bool {
+  // gave up.  wait() is called by a whole warp and answers all of it alike.
+  auto wait_one = [&](uint64_t* bar, uint32_t n, uint32_t limit) -> bool {
     uint32_t spins = 0;
     while (!mbar_try_wait(bar, n & 1u)) {
       if (*fail) return false;
@@ -316,13 +316,17 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
     }
     return true;
   };
-  // The builders, the products and the staging take job after job this way.
-  auto for_each_job = [&](auto&& fn, bool arrives) {
+  auto wait = [&](uint64_t* bar, uint32_t n, uint32_t limit) -> bool {
+    return __all_sync(0xffffffffu, wait_one(bar, n, limit));
+  };
+  // The builders and the staging take job after job this way.
+  auto for_each_job = [&](auto&& fn) {
     for (uint32_t i = 0;; ++i) {
       if (!wait(job_full + (i & 1u), i >> 1, kCommitLimit)) return;
       const Job& jb = jobs[i & 1u];
       if (jb.n < 0 || !fn(jb)) return;
-      if (arrives) mbar_arrive(job_empty + (i & 1u));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(job_empty + (i & 1u));
     }
   };
 
@@ -656,7 +660,7 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
         rp.next(stages);
       }
       return true;
-    }, lane == 0);
+    });
   } else if (warp < 16) {
     // ================================================================ value tiles
     const int bw = warp - 12;
@@ -721,7 +725,7 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
         rp.next(stages);
       }
       return true;
-    }, lane == 0);
+    });
   } else {
     if (warp == 16 && lane == 0) {
       // ============================================================== products
@@ -743,13 +747,13 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
                  accumulate || s > 0);
         if (last) tc_commit(o_done + stream);
       };
-      for_each_job([&](const Job& jb) -> bool {
+      auto products = [&](const Job& jb) -> bool {
         const int n = jb.n, ahead = dual ? 1 : 2;
         // (in the one-tile form the second stream reads the first one's tile)
-        if (!wait(q_full, nq, kCommitLimit)) return false;
+        if (!wait_one(q_full, nq, kCommitLimit)) return false;
         // the next key tile, once written
         auto key_tile = [&]() -> bool {
-          if (!wait(k_full + (nk & 1u), nk >> 1, kCommitLimit)) return false;
+          if (!wait_one(k_full + (nk & 1u), nk >> 1, kCommitLimit)) return false;
           tc_fence_after();
           return true;
         };
@@ -757,19 +761,19 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
           if (!key_tile()) return false;
           logits(dual ? 0 : i, nk & 1u);
           if (dual) {
-            if (!wait(q_full + 1, nq, kCommitLimit)) return false;
+            if (!wait_one(q_full + 1, nq, kCommitLimit)) return false;
             logits(1, nk & 1u);
           }
           tc_commit(k_empty + (nk & 1u));
           ++nk;
         }
-        if (dual && n == 0 && !wait(q_full + 1, nq, kCommitLimit)) return false;     // no phase is skipped
+        if (dual && n == 0 && !wait_one(q_full + 1, nq, kCommitLimit)) return false;     // no phase is skipped
         ++nq;
         for (int i = 0; i < n; ++i) {
           for (int x = 0; x < (dual ? 2 : 1); ++x) {
             const int stream = dual ? x : i & 1;
-            if (x == 0 && !wait(v_full + (nv & 1u), nv >> 1, kCommitLimit)) return false;
-            if (!wait(p_full + stream, stream ? np1 : np0, kCommitLimit)) return false;
+            if (x == 0 && !wait_one(v_full + (nv & 1u), nv >> 1, kCommitLimit)) return false;
+            if (!wait_one(p_full + stream, stream ? np1 : np0, kCommitLimit)) return false;
             if (stream) ++np1;
             else ++np0;
             tc_fence_after();
@@ -786,7 +790,12 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
           }
         }
         return true;
-      }, true);
+      };
+      for (uint32_t i = 0; wait_one(job_full + (i & 1u), i >> 1, kCommitLimit); ++i) {
+        const Job& jb = jobs[i & 1u];
+        if (jb.n < 0 || !products(jb)) break;
+        mbar_arrive(job_empty + (i & 1u));
+      }
     }
     if (warp == 17) {
       // ============================================================== staging
@@ -808,9 +817,10 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
           raise(g.error, PNMIX_DEVERR_PAGE);
           return 0;
         };
+        if (jb.b == g.skip_seq) return false;      // the test hook: what waits for these pages gives up
         int id = page_of(0);
         for (int i = 0; i < n; ++i, ++nr) {
-          if (nr >= stages && !__all_sync(0xffffffffu, wait(ring_empty + rp.stage, rp.phase - 1, kCommitLimit))) return false;
+          if (nr >= stages && !wait(ring_empty + rp.stage, rp.phase - 1, kCommitLimit)) return false;
           const int tok = first + i * (kTile / 2) + (lane << per_copy);
           // blocks of the half (the second half of a last tile may have none) and of this lane's copy
           const int blocks = max(0, min(4, (most - first - i * (kTile / 2) + 15) >> 4));
@@ -832,12 +842,12 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
           rp.next(stages);
         }
         return true;
-      }, lane == 0);
+      });
       // every staged copy lands before the CTA's shared memory is given up
       for (uint32_t k = 0; k < stages && k < nr; ++k) {
         const uint32_t last = (nr - 1 - k) / stages;      // phase of the stage's last use
         uint64_t* bar = ring_full + (nr - 1 - k) % stages;
-        for (uint32_t spins = 0; spins < g.wait_limit && !mbar_try_wait(bar, last & 1u); ++spins) {
+        for (uint32_t spins = 0; spins < kCommitLimit && !mbar_try_wait(bar, last & 1u); ++spins) {
         }
       }
     }
@@ -845,7 +855,7 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
       // ============================================================== the pieces of work
       uint32_t i = 0;
       auto give = [&](const Job& jb) -> bool {
-        if (i >= 2 && !wait(job_empty + (i & 1u), (i >> 1) - 1, kCommitLimit)) return false;
+        if (i >= 2 && !wait_one(job_empty + (i & 1u), (i >> 1) - 1, kCommitLimit)) return false;
         jobs[i & 1u] = jb;
         mbar_arrive(job_full + (i & 1u));
         ++i;

@@ -149,7 +149,7 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
       const bool two = tile_seen - tok > kBlock;
       const uint32_t slot = nis % kStages;
       uint8_t* dst = ring + slot * kStageBytes;
-      if (lane == 0) {
+      if (lane == 0 && pc.b != g.skip_seq) {
         const uint8_t* src = head_pages + p0 * page_bytes + static_cast<size_t>((tok & ((1 << page_shift) - 1)) >> 4) * BB;
         const bool split = two && page_shift == 4;
         const uint32_t n0 = two && !split ? 2 * BB : BB;

@@ -90,6 +90,7 @@ SIGNATURES = {
     "pnmix_kv4_read": (_i, [_CP, _BP, _KP, _RP, _RP, _vp]),
     "pnmix_kv4_workspace_bytes": (_sz, [_CP, _BP]),
     "pnmix_kv4_attention": (_i, [_CP, _BP, _RP, _KP, _RP, _vp, _sz, _vp]),
+    "pnmix_debug_kv4_stall": (_i, [_CP, _BP, _RP, _KP, _RP, _vp, _sz, _i, ctypes.c_uint32, _vp]),
     "pnmix_kv4_read_error": (_i, [_KP, _i, _P(ctypes.c_uint32)]),
 }
 for _name, (_res, _args) in SIGNATURES.items():
@@ -158,23 +159,36 @@ def _on(device, stream):
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
-def norm_rope(rope: Rope, q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, q_weight=None, k_weight=None,
-              q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+def norm_rope(rope: Rope, q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor, q_weight=None,
+              k_weight=None, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
     """Norm of every head of q and k (where a weight is given) and rotation by position.
-    q, k bf16 [n][heads][head_dim]; positions int32 [n_axes][n] ([n] with one axis).  Returns
-    (q_out, k_out), which may be the inputs themselves."""
-    dev, D = q.device, rope.head_dim
-    sq, sk = (q.shape[0], q.shape[1], D), (q.shape[0], k.shape[1], D)
-    rq, rk = _rows(q, sq, dev, "q"), _rows(k, sk, dev, "k")
-    pos = _positions(positions, rope.n_axes, sq[0], dev)
-    wq, wk = _weight(q_weight, D, dev, "q_weight"), _weight(k_weight, D, dev, "k_weight")
+    q, k bf16 [n][heads][head_dim], one of them may be None; positions int32 [n_axes][n] ([n]
+    with one axis).  Returns (q_out, k_out), which may be the inputs themselves."""
+    any_ = q if q is not None else k
+    if not isinstance(any_, torch.Tensor) or any_.dim() != 3:
+        raise TypeError("q and k are tensors [tokens][heads][head_dim], or one of them None")
+    dev, n, D = any_.device, any_.shape[0], rope.head_dim
+    pos = _positions(positions, rope.n_axes, n, dev)
+    rq = rk = oq = ok = None
+    hq = hk = 0
     ctx, s = _on(dev, stream)
     with ctx:
-        q_out = q.new_empty(sq) if q_out is None else q_out
-        k_out = k.new_empty(sk) if k_out is None else k_out
-        _check(_norm_rope(_byref(rope), sq[0], sq[1], sk[1], _byref(rq), _byref(rk), wq, wk, pos,
-                          _byref(_rows(q_out, sq, dev, "q_out")), _byref(_rows(k_out, sk, dev, "k_out")), s),
-               "pnmix_norm_rope")
+        if q is not None:
+            hq = q.shape[1]
+            shape = (n, hq, D)
+            rq = _byref(_rows(q, shape, dev, "q"))
+            q_out = q.new_empty(shape) if q_out is None else q_out
+            oq = _byref(_rows(q_out, shape, dev, "q_out"))
+        if k is not None:
+            if k.dim() != 3:
+                raise ValueError("k must be [tokens][heads][head_dim]")
+            hk = k.shape[1]
+            shape = (n, hk, D)
+            rk = _byref(_rows(k, shape, dev, "k"))
+            k_out = k.new_empty(shape) if k_out is None else k_out
+            ok = _byref(_rows(k_out, shape, dev, "k_out"))
+        _check(_norm_rope(_byref(rope), n, hq, hk, rq, rk, _weight(q_weight, D, dev, "q_weight"),
+                          _weight(k_weight, D, dev, "k_weight"), pos, oq, ok, s), "pnmix_norm_rope")
     return q_out, k_out
 
 

@@ -711,6 +711,18 @@ PNMIX_API pnmix_status pnmix_kv4_attention(const pnmix_kv4_config* cfg, const pn
                                            const pnmix_rows* out, void* workspace, size_t workspace_bytes,
                                            void* stream);
 
+/*
+ * Test hook of the bounded waits: pnmix_kv4_attention where the pages of sequence skip_seq are
+ * never staged and waits for staged pages give up after wait_rounds (>= 1) rounds of mbarrier
+ * try_wait.  Raises PNMIX_DEVERR_TIMEOUT; the output is then invalid (with up to 16 query rows
+ * per KV head, that of the other sequences is too where they share a CTA), while the cache and
+ * the CUDA context stay usable.
+ */
+PNMIX_API pnmix_status pnmix_debug_kv4_stall(const pnmix_kv4_config* cfg, const pnmix_kv4_batch* batch,
+                                             const pnmix_rows* q, const pnmix_kv4_cache* cache,
+                                             const pnmix_rows* out, void* workspace, size_t workspace_bytes,
+                                             int skip_seq, uint32_t wait_rounds, void* stream);
+
 /* pnmix_read_error for this cache. */
 PNMIX_API pnmix_status pnmix_kv4_read_error(const pnmix_kv4_cache* cache, int clear, uint32_t* host_error);
 

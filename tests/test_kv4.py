@@ -489,3 +489,98 @@ def test_two_streams_at_once(pm):
     torch.cuda.synchronize()
     for i, (_, _, want) in enumerate(sets):
         assert all(torch.equal(g, want) for g in got[i])
+
+
+# ---------------------------------------------------------------- the mixed-precision cache's own path
+
+def test_projected_prefill_and_steps_equal_the_separate_calls(pm):
+    B, Hq, Hkv, L, D, steps = 2, 8, 2, 100, 128, 3
+    G = Hq // Hkv
+    x = dev(rows(131, B * (L + steps), Hq + 2 * Hkv, D)).view(B, L + steps, Hq + 2 * Hkv, D)
+    w = [dev(ref.bf16(1 + 0.2 * np.random.default_rng(i).standard_normal(D))) for i in range(2)]
+    rope = pm.Rope.make(D, axes=axes_of(D, 3))
+    pos = torch.randint(0, 3000, (B, 3, L + steps), dtype=torch.int32, device=DEV)
+    cfg = pm.Config.make(Hq, Hkv)
+    a, b = (pm.PNMixCache(cfg, B, 128) for _ in range(2))
+    q, k, v = x.split([Hq, Hkv, Hkv], 2)
+    k_rot = a.prefill_projected(rope, q[:, :L], k[:, :L], v[:, :L], pos[:, :, :L].contiguous(), *w)
+    flat = pos.transpose(0, 1).reshape(3, -1).contiguous()
+    qr, kr = pm.norm_rope(rope, q.flatten(0, 1), k.flatten(0, 1), flat, *w)
+    qr, kr = qr.view(B, L + steps, Hq, D), kr.view(B, L + steps, Hkv, D)
+    hm = lambda t: t.transpose(1, 2).contiguous()  # noqa: E731
+    b.prefill(hm(qr[:, L - 64:L]), hm(kr[:, :L]), hm(v[:, :L]), L)
+    assert torch.equal(k_rot, hm(kr[:, :L])) and torch.equal(a.buffer, b.buffer)
+    for i in range(L, L + steps):
+        got = a.step_projected(rope, q[:, i], k[:, i], v[:, i], pos[:, :, i].t().contiguous(), *w)
+        want = torch.empty(B, Hq, D, dtype=torch.float32, device=DEV)
+        pm.pnmix_append_decode(cfg, kr[:, i].contiguous(), v[:, i].contiguous(), qr[:, i].contiguous(), b, want)
+        assert torch.equal(got, want) and torch.equal(a.buffer, b.buffer)
+    assert G * Hkv == Hq
+
+
+def test_norm_rope_of_one_side(pm):
+    n, D = 21, 128
+    q, k = dev(rows(141, n, 3, D)), dev(rows(142, n, 2, D))
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    rope = pm.Rope.make(D)
+    qo, ko = pm.norm_rope(rope, q, k, pos)
+    assert torch.equal(pm.norm_rope(rope, q, None, pos)[0], qo) and torch.equal(pm.norm_rope(rope, None, k, pos)[1], ko)
+    with pytest.raises(TypeError):
+        pm.norm_rope(rope, None, None, pos)
+
+
+# ---------------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("Hq,T", [(8, 1), (8, 40), (8, 140)])
+def test_a_staging_wait_that_runs_out_sets_the_error_bit(pm, Hq, T):
+    """One row tile of 8 rows, one of 128 and two of 128: the call returns, and the next one is right."""
+    import ctypes
+    from decode_attention_prefill_b200 import kv4
+    s = Setup(pm, [400, 300, 500], [T] * 3, Hq, 2, 128, 32)
+    s.fill()
+    q = dev(rows(151, s.n, Hq, 128))
+    want = s.cache.attend(s.batch, q)
+    out = torch.empty_like(q)
+    ws = torch.empty(pm.kv4_workspace_bytes(s.cfg, s.batch), dtype=torch.uint8, device=DEV)
+    shape, B = (s.n, Hq, 128), ctypes.byref
+    st = pm._lib.pnmix_debug_kv4_stall(B(s.cfg), s.batch.ref, B(kv4._rows(q, shape, q.device, "q")), B(s.cache.c),
+                                       B(kv4._rows(out, shape, q.device, "out")), ws.data_ptr(), ws.numel(), 1, 200,
+                                       torch.cuda.current_stream().cuda_stream)
+    assert st == pm.OK
+    assert s.cache.read_error() & pm.DEVERR_TIMEOUT
+    assert torch.equal(s.cache.attend(s.batch, q, workspace=ws), want) and s.cache.read_error() == 0
+
+
+def test_quantiser_on_many_values(pm):
+    """Bit-exact on a million values: offsets far above the range, ranges of a few bf16 steps,
+    powers of two (exact half-way codes), tiny numbers and zeros."""
+    r = np.random.default_rng(161)
+    n, H, D = 2000, 2, 128
+    x = r.standard_normal((n, H, D)) * np.exp(r.uniform(-12, 10, (n, H, 1))) + \
+        r.choice([0, 1, -1, 30, -300, 20000], (n, H, 1)) * r.uniform(0.5, 2, (n, H, 1))
+    x[::7] = r.integers(-40, 40, (len(x[::7]), H, D)) * 0.125
+    x[1::11] *= 2.0 ** -30
+    x[2::13, :, ::3] = 0
+    x = ref.bf16(np.where(np.abs(x) > 61440, 0, x)) + np.float32(0)        # no negative zeros
+    s = Setup(pm, [n], [n], 2, H, D, 64)
+    s.cache.append(s.batch, dev(x), dev(x[:, :, ::-1]))
+    k, v = s.cache.read(s.batch)
+    assert np.array_equal(host(k), ref.bf16_from_f32(ref.stand_for(*ref.quantise(x))))
+    assert np.array_equal(host(v), ref.bf16_from_f32(ref.stand_for(*ref.quantise(x[:, :, ::-1]))))
+    want = ref.Pages(s.n_pages, H, D, 64, s.raw())
+    for i in r.integers(0, n, 60):
+        for side, y in enumerate((x, x[:, :, ::-1])):
+            c, sc, z = ref.quantise(y[i])
+            want.put(s.table[0, i // 64], i % 64, side, c, sc, z)
+    assert np.array_equal(s.raw(), want.raw)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,T,lens", [
+    (128, 8, 2, 3, [5, 900, 17, 260]), (128, 8, 2, 9, [1000, 300, 9, 64]), (64, 12, 2, 30, [999, 30, 128, 511]),
+    (128, 4, 4, 129, [129, 1290, 500]), (64, 4, 1, 70, [70, 640, 71]), (128, 8, 1, 257, [1500])])
+def test_rows_of_both_tile_forms(pm, D, Hq, Hkv, T, lens):
+    """8, 16, 128 and 256 rows per tile, tiles that end inside a token, units shared by CTAs."""
+    s = Setup(pm, lens, [min(T, n) for n in lens], Hq, Hkv, D, 16)
+    s.fill(171)
+    q = rows(172, s.n, Hq, D)
+    s.check_attention(q, s.cache.attend(s.batch, dev(q)))

@@ -132,6 +132,9 @@ def test_workspace_cache_and_rope_refusals():
     assert att(None, need) == pm.ERR_INVALID_ARG
     assert att(ctypes.c_void_p(P + 16), need) == pm.ERR_ALIGNMENT
     assert att(ctypes.c_void_p(P), need - 1) == pm.ERR_CAPACITY
+    stall = lambda seq, rounds: L.pnmix_debug_kv4_stall(B(cfg), B(b), B(q), B(c), B(q), ctypes.c_void_p(P), need, seq,  # noqa: E731
+                                                        rounds, None)
+    assert stall(-1, 5) == stall(2, 5) == stall(0, 0) == pm.ERR_INVALID_ARG
     other = cache(pm.KV4Config.make(8, 4))
     assert L.pnmix_kv4_append(B(cfg), B(b), B(k), B(k), B(other), None) == pm.ERR_INVALID_ARG
     assert L.pnmix_kv4_append(B(cfg), B(b), B(k), B(k), None, None) == pm.ERR_INVALID_ARG
