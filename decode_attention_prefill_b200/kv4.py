@@ -146,17 +146,25 @@ _SAME = contextlib.nullcontext()
 
 
 def _on(device, stream):
-    """(context, raw stream): where a call on `device` goes.  Outputs made inside the context
-    belong to that stream."""
+    """(context, raw stream, stream object or None): where a call on `device` goes.  Outputs made
+    inside the context belong to that stream."""
     if stream is None:
         # the raw handle: a Stream object around it costs more than the rest of a small call
         ctx = _SAME if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        return ctx, torch._C._cuda_getCurrentRawStream(device.index)
+        return ctx, torch._C._cuda_getCurrentRawStream(device.index), None
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    return torch.cuda.stream(stream), stream.cuda_stream
+    return torch.cuda.stream(stream), stream.cuda_stream, stream
+
+
+def _used_on(stream, *tensors):
+    """Tells the allocator that a named stream uses these: their memory is not given out again
+    before it is done with them."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def norm_rope(rope: Rope, q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor, q_weight=None,
@@ -171,7 +179,7 @@ def norm_rope(rope: Rope, q: torch.Tensor | None, k: torch.Tensor | None, positi
     pos = _positions(positions, rope.n_axes, n, dev)
     rq = rk = oq = ok = None
     hq = hk = 0
-    ctx, s = _on(dev, stream)
+    ctx, s, named = _on(dev, stream)
     with ctx:
         if q is not None:
             hq = q.shape[1]
@@ -189,6 +197,8 @@ def norm_rope(rope: Rope, q: torch.Tensor | None, k: torch.Tensor | None, positi
             ok = _byref(_rows(k_out, shape, dev, "k_out"))
         _check(_norm_rope(_byref(rope), n, hq, hk, rq, rk, _weight(q_weight, D, dev, "q_weight"),
                           _weight(k_weight, D, dev, "k_weight"), pos, oq, ok, s), "pnmix_norm_rope")
+    if named is not None:
+        _used_on(named, q, k, positions, q_weight, k_weight, q_out, k_out)
     return q_out, k_out
 
 
@@ -239,23 +249,30 @@ class KV4Cache:
 
     def reset(self, stream=None):
         """Zero the pages and the error word."""
-        ctx, s = _on(self.device, stream)
+        ctx, s, named = _on(self.device, stream)
         with ctx:
             _check(_lib.pnmix_kv4_cache_reset(self._refs[1], s), "pnmix_kv4_cache_reset")
+        if named is not None:
+            _used_on(named, self.buffer)
 
     def _on(self, batch: KV4Batch, stream):
         if batch.device != self.device:
             raise ValueError(f"the batch is on {batch.device}, the cache on {self.device}")
         return _on(self.device, stream)
 
+    def _used_on(self, stream, batch: KV4Batch, *tensors):
+        _used_on(stream, self.buffer, batch.kv_len, batch.page_table, batch.q_start, *tensors)
+
     def append(self, batch: KV4Batch, k: torch.Tensor, v: torch.Tensor, stream=None):
         """Quantise rows k, v bf16 [n][Hkv][head_dim] (after RoPE) into the batch's places."""
         kv = (batch.n_tokens, *self._kv)
         rk, rv = _rows(k, kv, self.device, "k"), _rows(v, kv, self.device, "v")
-        ctx, s = self._on(batch, stream)
+        ctx, s, named = self._on(batch, stream)
         with ctx:
             _check(_lib.pnmix_kv4_append(self._refs[0], batch.ref, _byref(rk), _byref(rv), self._refs[1], s),
                    "pnmix_kv4_append")
+        if named is not None:
+            self._used_on(named, batch, k, v)
 
     def append_qkv(self, batch: KV4Batch, rope: Rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                    positions: torch.Tensor, q_weight=None, k_weight=None, q_out: torch.Tensor | None = None,
@@ -267,25 +284,29 @@ class KV4Cache:
         pos = _positions(positions, rope.n_axes, n, dev)
         D = qs[2]
         wq, wk = _weight(q_weight, D, dev, "q_weight"), _weight(k_weight, D, dev, "k_weight")
-        ctx, s = self._on(batch, stream)
+        ctx, s, named = self._on(batch, stream)
         with ctx:
             q_out = q.new_empty(qs) if q_out is None else q_out
             _check(_lib.pnmix_kv4_append_qkv(self._refs[0], _byref(rope), batch.ref, _byref(rq), _byref(rk),
                                              _byref(rv), wq, wk, pos, _byref(_rows(q_out, qs, dev, "q_out")),
                                              self._refs[1], s), "pnmix_kv4_append_qkv")
+        if named is not None:
+            self._used_on(named, batch, q, k, v, positions, q_weight, k_weight, q_out)
         return q_out
 
     def read(self, batch: KV4Batch, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
              stream=None):
         """The batch's rows as the cache holds them: (k, v) bf16 [n][Hkv][head_dim]."""
         kv, dev = (batch.n_tokens, *self._kv), self.device
-        ctx, s = self._on(batch, stream)
+        ctx, s, named = self._on(batch, stream)
         with ctx:
             k_out = torch.empty(kv, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
             v_out = torch.empty_like(k_out) if v_out is None else v_out
             _check(_lib.pnmix_kv4_read(self._refs[0], batch.ref, self._refs[1],
                                        _byref(_rows(k_out, kv, dev, "k_out")),
                                        _byref(_rows(v_out, kv, dev, "v_out")), s), "pnmix_kv4_read")
+        if named is not None:
+            self._used_on(named, batch, k_out, v_out)
         return k_out, v_out
 
     def attend(self, batch: KV4Batch, q: torch.Tensor, out: torch.Tensor | None = None,
@@ -295,7 +316,7 @@ class KV4Cache:
         one is given."""
         qs, dev = (batch.n_tokens, *self._q), self.device
         rq = _rows(q, qs, dev, "q")
-        ctx, s = self._on(batch, stream)
+        ctx, s, named = self._on(batch, stream)
         with ctx:
             out = q.new_empty(qs) if out is None else out
             if workspace is None:
@@ -306,6 +327,8 @@ class KV4Cache:
             _check(_lib.pnmix_kv4_attention(self._refs[0], batch.ref, _byref(rq), self._refs[1],
                                             _byref(_rows(out, qs, dev, "out")), workspace.data_ptr(),
                                             workspace.numel(), s), "pnmix_kv4_attention")
+        if named is not None:
+            self._used_on(named, batch, q, out, workspace)
         return out
 
     def pages(self) -> torch.Tensor:

@@ -584,3 +584,82 @@ def test_rows_of_both_tile_forms(pm, D, Hq, Hkv, T, lens):
     s.fill(171)
     q = rows(172, s.n, Hq, D)
     s.check_attention(q, s.cache.attend(s.batch, dev(q)))
+
+
+def test_offsets_past_32_bits(pm):
+    """Pages whose bytes lie more than 4 GiB behind the first."""
+    D, Hq, Hkv, page = 128, 8, 8, 128
+    cfg = pm.KV4Config.make(Hq, Hkv, D, page)
+    n_pages = (5 << 30) // (Hkv * page * 20 * D // 16)
+    cache = pm.KV4Cache(cfg, n_pages)
+    table = np.array([[n_pages - 1, 3, n_pages - 2], [n_pages - 3, n_pages - 4, 0]], np.int32)
+    lens = [300, 260]
+    n = sum(lens)
+    whole = pm.KV4Batch(dev(np.array(lens), torch.int32), dev(table, torch.int32),
+                        dev(np.array([0, lens[0], n]), torch.int32), n_tokens=n)
+    k, v = dev(rows(181, n, Hkv, D)), dev(rows(182, n, Hkv, D))
+    cache.append(whole, k, v)
+    ko, vo = cache.read(whole)
+    assert np.array_equal(host(ko), ref.bf16_from_f32(ref.stand_for(*ref.quantise(host(k)))))
+    assert np.array_equal(host(vo), ref.bf16_from_f32(ref.stand_for(*ref.quantise(host(v)))))
+    small = pm.KV4Cache(cfg, 6)          # the same tokens in a small cache give the same bits
+    near = pm.KV4Batch(whole.kv_len, dev(np.arange(6).reshape(2, 3), torch.int32), whole.q_start, n_tokens=n)
+    small.append(near, k, v)
+    for T in (1, 60):
+        q = dev(rows(183, 2 * T, Hq, D))
+        a = cache.attend(pm.KV4Batch(whole.kv_len, whole.page_table, n_tokens=2 * T), q)
+        b = small.attend(pm.KV4Batch(whole.kv_len, near.page_table, n_tokens=2 * T), q)
+        assert torch.equal(a, b)
+
+
+def test_more_rows_than_max_q_is_an_error(pm):
+    s = Setup(pm, [50, 60], [3, 7], 4, 2, 64, 16)
+    s.fill()
+    q = dev(rows(191, s.n, 4, 64))
+    out = torch.full_like(q, 4.0)
+    s.cache.attend(s.make_batch(s.kv_len, s.start, max_q=6), q, out=out)
+    assert s.cache.read_error() == pm.DEVERR_BATCH and (out == 4).all()
+
+
+def test_inputs_of_a_named_stream_may_be_dropped(pm):
+    """Memory of tensors that another stream still reads is not handed out again."""
+    s = Setup(pm, [3000] * 4, [1] * 4, 8, 2, 128, 64)
+    s.fill()
+    side = torch.cuda.Stream()
+    q = rows(193, s.n, 8, 128)
+    want = s.cache.attend(s.batch, dev(q))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+        t = dev(q)
+        side.wait_stream(torch.cuda.current_stream())
+        out = s.cache.attend(s.batch, t, stream=side)
+        del t
+        torch.full((s.n, 8, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+        side.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_the_same_workspace_in_two_graphs(pm):
+    """Two graphs that were captured with one workspace, replayed in turn."""
+    sets = []
+    a = Setup(pm, [900, 400], [1, 1], 8, 2, 128, 32)
+    b = Setup(pm, [300, 800], [30, 30], 8, 2, 128, 32, seed=3)
+    need = max(pm.kv4_workspace_bytes(x.cfg, x.batch) for x in (a, b))
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    for s in (a, b):
+        s.fill(195)
+        q = dev(rows(196, s.n, 8, 128))
+        want = s.cache.attend(s.batch, q)
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            out = s.cache.attend(s.batch, q, workspace=ws)
+        sets.append((g, out, want, q))          # a replay reads q where it was captured
+    for i in range(6):
+        g, out, want, _ = sets[i % 2]
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
