@@ -21,7 +21,7 @@
 //            accumulators are rescaled a few times per run.
 //   values   A = value codes, 16 channels x 16 tokens; two tokens' words are joined by a byte
 //            permute and masked like the keys.  B = p * s_v per channel group, rounded once to
-//            fp16 (2^-12 of each weight at most) and transposed by movmatrix from the logits'
+//            fp16 (2^-11 of each weight at most) and transposed by movmatrix from the logits'
 //            register layout.  The zero points add sum(p * z_v) per group in fp32.
 //
 // The token that row i of an A tile holds is i / 2 for even i < 8 and 7 - i / 2 for odd (and 8
