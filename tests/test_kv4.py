@@ -663,3 +663,24 @@ def test_the_same_workspace_in_two_graphs(pm):
         out.zero_()
         g.replay()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("B,T", [(40, 1), (12, 20)])
+def test_waits_of_one_round(pm, B, T):
+    """Nearly every wait gives up at once, with copies in flight: the call returns, and the next
+    ones are right."""
+    import ctypes
+    from decode_attention_prefill_b200 import kv4
+    s = Setup(pm, [700 + 13 * i for i in range(B)], [T] * B, 8, 2, 128, 16)
+    s.fill()
+    q = dev(rows(211, s.n, 8, 128))
+    want = s.cache.attend(s.batch, q)
+    out = torch.empty_like(q)
+    ws = torch.empty(pm.kv4_workspace_bytes(s.cfg, s.batch), dtype=torch.uint8, device=DEV)
+    shape, ref_ = (s.n, 8, 128), ctypes.byref
+    for seq in (0, B // 2, B - 1):
+        st = pm._lib.pnmix_debug_kv4_stall(ref_(s.cfg), s.batch.ref, ref_(kv4._rows(q, shape, q.device, "q")),
+                                           ref_(s.cache.c), ref_(kv4._rows(out, shape, q.device, "out")), ws.data_ptr(),
+                                           ws.numel(), seq, 1, torch.cuda.current_stream().cuda_stream)
+        assert st == pm.OK and s.cache.read_error() & pm.DEVERR_TIMEOUT
+        assert torch.equal(s.cache.attend(s.batch, q, workspace=ws), want) and s.cache.read_error() == 0
