@@ -576,21 +576,26 @@ merge_kernel(const __grid_constant__ AttnArgs a, int RT) {
 
 constexpr int kMaxDevices = 64;
 
-// CTAs that fit the current device at once.
+// CTAs that fit the current device at once; for up to 1024 sequences and for more, whose plan
+// leaves room for one CTA less (the answer must not depend on what was called first).
 template <int D, int NT>
-cudaError_t wave_of(size_t smem, int* wave) {
-  static std::atomic<int> cache[kMaxDevices];
+cudaError_t wave_of(int batch, int* wave) {
+  constexpr int kSmall = 1024;
+  static std::atomic<int> caches[2][kMaxDevices];
+  std::atomic<int>* cache = caches[batch > kSmall];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const bool known = dev >= 0 && dev < kMaxDevices;
   if (known && (*wave = cache[dev].load(std::memory_order_relaxed)) != 0) return cudaSuccess;
   auto kern = decode_kernel<D, NT>;
-  const int most = static_cast<int>(kWarps * kStages * 40 * D + plan_bytes(kMaxBatch));
+  const size_t ring = kWarps * kStages * 40 * D;
+  const int most = static_cast<int>(ring + plan_bytes(kMaxBatch));
   int sms = 0, per = 0;
   if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess ||
       (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
-      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, kThreads, smem)) != cudaSuccess)
+      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+           &per, kern, kThreads, ring + plan_bytes(batch > kSmall ? kMaxBatch : kSmall))) != cudaSuccess)
     return e;
   *wave = sms * (per > 0 ? per : 1);
   if (known) cache[dev].store(*wave, std::memory_order_relaxed);
@@ -632,7 +637,7 @@ template <int D, int NT>
 static cudaError_t launch_rows(const AttnArgs& a, int* ctas, cudaStream_t s) {
   const size_t smem = kWarps * kStages * 40 * D + plan_bytes(a.bt.B);
   int wave = 0;
-  const cudaError_t e = wave_of<D, NT>(smem, &wave);
+  const cudaError_t e = wave_of<D, NT>(a.bt.B, &wave);
   if (e != cudaSuccess) return e;
   *ctas = wave < kMaxCtas ? wave : kMaxCtas;
   decode_kernel<D, NT><<<*ctas, kThreads, smem, s>>>(a);

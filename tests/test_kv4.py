@@ -684,3 +684,33 @@ def test_waits_of_one_round(pm, B, T):
                                            ws.numel(), seq, 1, torch.cuda.current_stream().cuda_stream)
         assert st == pm.OK and s.cache.read_error() & pm.DEVERR_TIMEOUT
         assert torch.equal(s.cache.attend(s.batch, q, workspace=ws), want) and s.cache.read_error() == 0
+
+
+def test_the_answer_does_not_depend_on_earlier_calls(pm):
+    """The split of the work follows from the call: a first call with very many sequences (whose
+    launch leaves less room on the GPU) changes no bit of a later one."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import sys, hashlib, torch
+import decode_attention_prefill_b200 as pm
+torch.manual_seed(5)
+cfg = pm.KV4Config.make(16, 4, 128, 64)
+cache = pm.KV4Cache(cfg, 400)
+i32 = dict(dtype=torch.int32, device="cuda")
+k = torch.randn(4 * 6400, 4, 128, device="cuda").bfloat16()
+table = torch.arange(400, **i32).view(4, 100)
+full = torch.full((4,), 6400, **i32)
+cache.append(pm.KV4Batch(full, table, n_tokens=4 * 6400), k, k)
+q = torch.randn(2048, 16, 128, device="cuda").bfloat16()
+if sys.argv[1] == "many":
+    cache.attend(pm.KV4Batch(torch.full((2048,), 64, **i32), table.view(-1)[:1].repeat(2048).view(2048, 1), n_tokens=2048), q)
+out = cache.attend(pm.KV4Batch(full, table, n_tokens=4), q[:4].contiguous())
+print(hashlib.sha256(out.cpu().view(torch.int16).numpy().tobytes()).hexdigest())
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(pm.__file__)))
+    got = [subprocess.run([sys.executable, "-c", code, how], cwd=root, capture_output=True, text=True, timeout=300)
+           for how in ("many", "alone")]
+    assert all(g.returncode == 0 for g in got), got
+    assert got[0].stdout == got[1].stdout
