@@ -389,10 +389,13 @@ class PNMixCache:
         before norm and rotation, positions int32 [B][n_axes][L] ([B][L] with one axis).  Every
         head is normed (where a weight is given) and rotated by norm_rope, straight into the
         head-major tensors that prefill takes.  Returns the rotated keys, [B][Hkv][L][128]."""
-        from .kv4 import _on
-        B, L, Hq, D = q.shape
+        from .kv4 import _on, _used_on
+        L = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 4 else 0
+        self._check_projected(q, k, v, (self.batch, L))
+        B, Hq, D = q.shape[0], q.shape[2], q.shape[3]
         W = min(L, self.cfg.saliency_window)
-        with _on(q.device, stream)[0]:
+        ctx, _, named = _on(q.device, stream)
+        with ctx:
             q_win = q.new_empty(B, Hq, W, D)
             k_rot = k.new_empty(B, k.shape[2], L, D)
             pos = positions.view(B, -1, L)
@@ -401,7 +404,20 @@ class PNMixCache:
                           q_out=q_win[b].transpose(0, 1))
                 norm_rope(rope, None, k[b], pos[b].contiguous(), None, k_weight, k_out=k_rot[b].transpose(0, 1))
             self.prefill(q_win, k_rot, v.transpose(1, 2).contiguous(), L)
+        if named is not None:
+            _used_on(named, q, k, v, positions, q_weight, k_weight, self.buffer)
         return k_rot
+
+    def _check_projected(self, q, k, v, lead):
+        """Refuses projections that are not [*lead][heads][128] of this cache, on its device."""
+        cfg = self.cfg
+        for name, t, heads in (("q", q, cfg.n_q_heads), ("k", k, cfg.n_kv_heads), ("v", v, cfg.n_kv_heads)):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+                raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
+            if t.shape != (*lead, heads, cfg.head_dim):
+                raise ValueError(f"{name} must be {[*lead, heads, cfg.head_dim]}, got {list(t.shape)}")
+            if t.device != self.buffer.device:
+                raise ValueError(f"{name} is on {t.device}, the cache on {self.buffer.device}")
 
     def append(self, k_new, v_new, stream=None):
         pnmix_append(self.cfg, k_new, v_new, self, stream)
@@ -410,11 +426,17 @@ class PNMixCache:
         """One decode step from a model's projections: q bf16 [B][Hq][128], k, v bf16 [B][Hkv][128]
         before norm and rotation (views of one projection, say), positions int32 [n_axes][B] ([B]
         with one axis).  norm_rope, then pnmix_append_decode: fp32 [B][Hq][128]."""
-        from .kv4 import _on
-        with _on(q.device, stream)[0]:
-            q, k = norm_rope(rope, q, k, positions, q_weight, k_weight)
+        from .kv4 import _on, _used_on
+        self._check_projected(q, k, v, (self.batch,))
+        if out is not None and (out.shape != q.shape or out.device != q.device):
+            raise ValueError(f"out must be {list(q.shape)} on {q.device}")
+        ctx, _, named = _on(q.device, stream)
+        with ctx:
+            q_rot, k_rot = norm_rope(rope, q, k, positions, q_weight, k_weight)
             out = torch.empty(q.shape, dtype=torch.float32, device=q.device) if out is None else out
-            pnmix_append_decode(self.cfg, k, v.contiguous(), q, self, out)
+            pnmix_append_decode(self.cfg, k_rot, v.contiguous(), q_rot, self, out)
+        if named is not None:
+            _used_on(named, q, k, v, positions, q_weight, k_weight, out, self.buffer, self.workspace)
         return out
 
     def shrunk(self, stream=None, max_queries: int = 1) -> "PNMixCache":

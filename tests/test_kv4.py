@@ -714,3 +714,28 @@ print(hashlib.sha256(out.cpu().view(torch.int16).numpy().tobytes()).hexdigest())
            for how in ("many", "alone")]
     assert all(g.returncode == 0 for g in got), got
     assert got[0].stdout == got[1].stdout
+
+
+def test_projected_calls_refuse_what_is_not_the_caches(pm):
+    cache = pm.PNMixCache(pm.Config.make(8, 2), 2, 128)
+    bf = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    rope, pos = pm.Rope.make(128), torch.zeros(2, 70, dtype=torch.int32, device=DEV)
+    good = bf(2, 70, 8, 128), bf(2, 70, 2, 128), bf(2, 70, 2, 128)
+    cache.prefill_projected(rope, *good, pos)
+    step, at = (bf(2, 8, 128), bf(2, 2, 128), bf(2, 2, 128)), pos[:, 0].contiguous()
+    cache.step_projected(rope, *step, at)
+    before = cache.buffer.clone()
+    for i, bad in [(0, bf(1, 70, 8, 128)), (0, bf(2, 70, 4, 128)), (1, bf(2, 69, 2, 128)), (2, bf(2, 70, 1, 128)),
+                   (2, bf(2, 70, 2, 64)), (0, bf(70, 8, 128))]:
+        with pytest.raises(ValueError):
+            cache.prefill_projected(rope, *[bad if i == j else t for j, t in enumerate(good)], pos)
+    for i, bad in [(0, bf(1, 8, 128)), (1, bf(2, 1, 128)), (2, bf(2, 2, 64)), (0, bf(2, 1, 8, 128))]:
+        with pytest.raises(ValueError):
+            cache.step_projected(rope, *[bad if i == j else t for j, t in enumerate(step)], at)
+    with pytest.raises(TypeError):
+        cache.step_projected(rope, step[0].float(), *step[1:], at)
+    with pytest.raises(ValueError):
+        cache.step_projected(rope, *step, at, out=torch.empty(1, 8, 128, device=DEV))
+    with pytest.raises(ValueError):
+        cache.step_projected(rope, *step, pos)
+    assert torch.equal(cache.buffer, before)
