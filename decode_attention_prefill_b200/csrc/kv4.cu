@@ -239,6 +239,7 @@ static pnmix_status attention(Geo g, const pnmix_kv4_batch* batch, const pnmix_r
   if (!workspace) return PNMIX_ERR_INVALID_ARG;
   if (!aligned(workspace, 256)) return PNMIX_ERR_ALIGNMENT;
   if (workspace_bytes < attention_workspace_bytes(g, bt)) return PNMIX_ERR_CAPACITY;
+  if (q->data == out->data) return PNMIX_ERR_INVALID_ARG;      // rows are read again after some are written
   return cuda_status(launch_attention(g, bt, *q, *out, workspace, static_cast<cudaStream_t>(stream)));
 }
 

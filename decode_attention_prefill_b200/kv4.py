@@ -204,7 +204,8 @@ def norm_rope(rope: Rope, q: torch.Tensor | None, k: torch.Tensor | None, positi
 
 class KV4Batch:
     """The sequences of one call (pnmix_kv4_batch).  The tensors are kept, not copied: their
-    contents may change between calls (and between replays of a graph).
+    contents may change between calls (and between replays of a graph).  Which tensors they are
+    and how many rows there are stays as it was made.
 
     kv_len int32 [B], the calls' rows included; page_table int32 [B][max_pages]; q_start
     int32 [B + 1], or None for n_tokens / B rows of every sequence.  n_tokens: rows of the
@@ -220,13 +221,15 @@ class KV4Batch:
         B, dev = kv_len.numel(), kv_len.device
         if max_q is None:
             max_q = n_tokens if q_start is not None else n_tokens // B
-        self.device, self.n_tokens = dev, n_tokens
-        self.kv_len, self.page_table, self.q_start = kv_len, page_table, q_start
-        self.c = _Batch(B, n_tokens, page_table.shape[1], max_q,
-                        None if q_start is None else _ints(q_start, (B + 1,), dev, "q_start"),
-                        _ints(kv_len, (B,), dev, "kv_len"),
-                        _ints(page_table, (B, page_table.shape[1]), dev, "page_table"))
-        self.ref = ctypes.byref(self.c)
+        c = _Batch(B, n_tokens, page_table.shape[1], max_q,
+                   None if q_start is None else _ints(q_start, (B + 1,), dev, "q_start"),
+                   _ints(kv_len, (B,), dev, "kv_len"),
+                   _ints(page_table, (B, page_table.shape[1]), dev, "page_table"))
+        self.__dict__.update(device=dev, n_tokens=n_tokens, kv_len=kv_len, page_table=page_table, q_start=q_start,
+                             c=c, ref=ctypes.byref(c))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name} of a KV4Batch stays as it was made; make another batch")
 
 
 class KV4Cache:
@@ -234,6 +237,7 @@ class KV4Cache:
     kv4_cache_bytes long (its contents stay); without it zeroed memory is taken."""
 
     def __init__(self, cfg: KV4Config, n_pages: int, device="cuda", buffer: torch.Tensor | None = None):
+        cfg = KV4Config.from_buffer_copy(cfg)      # what the caller does with theirs later changes no call
         self.cfg, self.n_pages = cfg, n_pages
         nbytes = kv4_cache_bytes(cfg, n_pages)
         if buffer is None:

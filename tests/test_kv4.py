@@ -739,3 +739,17 @@ def test_projected_calls_refuse_what_is_not_the_caches(pm):
     with pytest.raises(ValueError):
         cache.step_projected(rope, *step, pos)
     assert torch.equal(cache.buffer, before)
+
+
+def test_what_a_batch_and_a_cache_were_made_with_stays(pm):
+    s = Setup(pm, [40], [2], 8, 2, 128, 16)
+    s.fill()
+    q = dev(rows(201, 2, 8, 128))
+    want = s.cache.attend(s.batch, q)
+    for name, value in (("n_tokens", 200), ("kv_len", q), ("page_table", None), ("q_start", None)):
+        with pytest.raises(AttributeError):
+            setattr(s.batch, name, value)
+    s.cfg.n_q_heads, s.cfg.softmax_scale = 16, 9.0      # the caller's, no longer the cache's
+    assert torch.equal(s.cache.attend(s.batch, q), want)
+    with pytest.raises(pm.PNMixError):
+        s.cache.attend(s.batch, q, out=q)

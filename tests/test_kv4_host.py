@@ -132,6 +132,7 @@ def test_workspace_cache_and_rope_refusals():
     assert att(None, need) == pm.ERR_INVALID_ARG
     assert att(ctypes.c_void_p(P + 16), need) == pm.ERR_ALIGNMENT
     assert att(ctypes.c_void_p(P), need - 1) == pm.ERR_CAPACITY
+    assert att(ctypes.c_void_p(P), need) == pm.ERR_INVALID_ARG          # the output is the query tensor
     stall = lambda seq, rounds: L.pnmix_debug_kv4_stall(B(cfg), B(b), B(q), B(c), B(q), ctypes.c_void_p(P), need, seq,  # noqa: E731
                                                         rounds, None)
     assert stall(-1, 5) == stall(2, 5) == stall(0, 0) == pm.ERR_INVALID_ARG
