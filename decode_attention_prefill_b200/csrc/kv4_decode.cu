@@ -613,11 +613,16 @@ constexpr int kMaxCtas = 1024;
 //     against 394 us; 8 x 8K x 8 heads:  24 rows 70 against 72 us, 48 rows 98 against 73 us
 //   head_dim 64, 8 x 8K x 8 heads:  20 rows 48 against 68 us, 48 rows 66 against 68 us, 64 rows
 //     82 against 66 us
+// Where some sequence may have more than 128 rows the average says less.  16 against 256 rows, 4
+// rows per token and KV head, 8 heads:  64 tokens of 64 sequences, 4K cached, 127 against 363 us;
+// a chunk of 256 tokens at 8K among 127 single ones at 2K (12 rows on the average) 353 against
+// 437 us; but a chunk of 128 at 32K among 31 single ones at 512 (20 rows) 436 against 170 us, and
+// of 64 among 63 (8 rows) 244 against 153 us.  So up to 16, one tile of most sequences.
 static int tile_rows(const Geo& g, const Batch& bt) {
   const int most = g.G * bt.max_q;
   const double mean = static_cast<double>(g.G) * bt.n_tokens / bt.B;
   if (most <= 8) return 8;
-  if (most <= 16 || (most <= 128 && mean <= (g.D == 128 ? 24 : 48))) return 16;
+  if (most <= 16 || mean <= (most > 128 ? 16 : g.D == 128 ? 24 : 48)) return 16;
   return most <= 128 ? 128 : 256;
 }
 
