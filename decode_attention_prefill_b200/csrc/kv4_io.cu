@@ -12,7 +12,7 @@
 // shuffles and narrow stores: 123 us instead of 59 for 16384 tokens of 40 heads, and the
 // read-back, with integer conversions at a quarter of the rate, 96 us instead of 62 for
 // 2 x 32768 tokens of 8 heads.  These are 5.6 and 5.7 TB/s, 86 % of a plain copy; the write of
-// 16384 tokens of 8 + 8 heads takes 43 us, 4.1 TB/s or 62 %, and is held by its instructions.)
+// 16384 tokens of 8 + 8 heads takes 27 us, 3.3 TB/s or 50 %, and is held by its instructions.)
 // A warp's eight rows are eight tokens of a head where there are that many: their packed rows
 // lie side by side.  A token's angles (fp64 product, reduced to a turn, one sincospi per pair)
 // and its place in the cache are worked out once per CTA, while the first rows' loads are in
@@ -200,8 +200,12 @@ __host__ __device__ __forceinline__ int turn_stride(int half) { return 2 * half 
 
 // ROPE: q and k rows are normed and rotated.  QUANT: k and v rows go to the cache (otherwise
 // k rows are stored like q's).
+// CTAs per SM.  Rotating kernels: seven (72 registers) instead of the six that 80 leave room for,
+// the fused write of 3900 ragged tokens of 28 + 4 + 4 heads 22.2 against 24.2 us, the norm alone
+// the same 59.7 us; eight spill (25.1 and 64.6 us).  The plain write: eight (64 registers); ten
+// take 28.7 instead of 26.7 us.  256 channels: three, the registers that they need.
 template <int D, bool ROPE, bool QUANT, int PAIRS>
-__global__ void __launch_bounds__(kInThreads)
+__global__ void __launch_bounds__(kInThreads, D == 256 ? 3 : ROPE ? 7 : 8)
 rows_in_kernel(const __grid_constant__ IoArgs a) {
   constexpr int NG = D / 32;
   extern __shared__ __align__(16) float shared[];   // [token][cos, sin], then [warp][8 rows][D + 4]
