@@ -498,7 +498,12 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
 // CTA x takes the unit that begins in CTA x of the launch before, 8 rows of it (rows inner, as
 // the partials lie), and turns them around in shared memory
 // for the stores.
-template <int D>
+// AHEAD partials at a time, all of their loads first.  After the row kernels eight (108
+// registers): a unit has many partials and the merge is a few round trips (with four, 5 ragged
+// tokens of 8 sequences 36.9 instead of 35.6 us).  After the tcgen05 kernel, whose units have two
+// or three mostly but 128 or 256 rows, four (72 registers, seven CTAs per SM instead of four):
+// 2 x 1024 tokens over 8192 cached ones 314 instead of 319 us.
+template <int D, int AHEAD>
 __global__ void __launch_bounds__(kThreads)
 merge_kernel(const __grid_constant__ AttnArgs a, int RT) {
   constexpr int C4 = D / 4, kRows = 8, kLanes = kThreads / kRows;    // threads per row
@@ -510,18 +515,17 @@ merge_kernel(const __grid_constant__ AttnArgs a, int RT) {
   const int n = f.last - first + 1;
   const int v0 = blockIdx.y * kRows, r = threadIdx.x & (kRows - 1), c0 = threadIdx.x / kRows, v = v0 + r;
   if (v0 >= f.rows) return;
-  // kAhead partials at a time, all of their loads first: few partials are one round trip
-  constexpr int kAhead = 8, kC = C4 / kLanes;
+  constexpr int kC = C4 / kLanes;
   float m = -1e30f, l = 0.f;
   float4 o[kC];
 #pragma unroll
   for (int i = 0; i < kC; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (v < f.rows) {
-    for (int k0 = 0; k0 < n; k0 += kAhead) {
-      float2 x[kAhead];
-      float4 t[kAhead][kC];
+    for (int k0 = 0; k0 < n; k0 += AHEAD) {
+      float2 x[AHEAD];
+      float4 t[AHEAD][kC];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
+      for (int k = 0; k < AHEAD; ++k) {
         x[k] = make_float2(-1e30f, 0.f);
         if (k0 + k < n) {
           const float* p = part_of<D>(a.wk.part, slot_of(first + k0 + k, first), RT);
@@ -532,7 +536,7 @@ merge_kernel(const __grid_constant__ AttnArgs a, int RT) {
       }
       float top = m;
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
+      for (int k = 0; k < AHEAD; ++k)
         if (x[k].y != 0.f) top = fmaxf(top, x[k].x);      // a partial that saw nothing has l = 0
       const float old = ex2(m - top);
       m = top;
@@ -540,7 +544,7 @@ merge_kernel(const __grid_constant__ AttnArgs a, int RT) {
 #pragma unroll
       for (int i = 0; i < kC; ++i) o[i] = make_float4(o[i].x * old, o[i].y * old, o[i].z * old, o[i].w * old);
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
+      for (int k = 0; k < AHEAD; ++k) {
         if (x[k].y == 0.f) continue;
         const float w = ex2(x[k].x - m);
         l = fmaf(x[k].y, w, l);
@@ -661,7 +665,7 @@ static cudaError_t launch_merge(const AttnArgs& a, int ctas, int rt, cudaStream_
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, a, rt);
+  return rt > 16 ? cudaLaunchKernelEx(&cfg, merge_kernel<D, 4>, a, rt) : cudaLaunchKernelEx(&cfg, merge_kernel<D, 8>, a, rt);
 }
 
 cudaError_t launch_attention(const Geo& g, const Batch& bt, const pnmix_rows& q, const pnmix_rows& out, void* ws,
