@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import struct
 
 import torch
 
@@ -97,15 +98,30 @@ for _name, (_res, _args) in SIGNATURES.items():
     _fn = getattr(_lib, _name)
     _fn.restype = _res
     _fn.argtypes = _args
-_norm_rope, _byref = _lib.pnmix_norm_rope, ctypes.byref
+_byref = ctypes.byref
 
 
-def _rows(t: torch.Tensor, shape: tuple, device, name: str) -> _Rows:
-    """Pointer and strides of a bf16 tensor [tokens][heads][head_dim] on `device`."""
+def _untyped(name: str):
+    """The same call with its pointers to structures as plain addresses: a packed pnmix_rows passed as
+    bytes costs a quarter of a ctypes structure, and a small call is bound by such things (the
+    norm of one token 17.0 us a call, with structures and checks of its own outputs 20.6)."""
+    fn = _lib[name]
+    res, args = SIGNATURES[name]
+    fn.restype, fn.argtypes = res, [_vp if a in (_RP, _BP, _KP, _CP, _OP) else a for a in args]
+    return fn
+
+
+_norm_rope, _append, _append_qkv, _read, _attention = (_untyped("pnmix_" + n) for n in (
+    "norm_rope", "kv4_append", "kv4_append_qkv", "kv4_read", "kv4_attention"))
+_pack = struct.Struct("Pqq").pack        # pnmix_rows
+
+
+def _strides(t: torch.Tensor, shape: tuple, device, name: str) -> tuple:
+    """The fields of pnmix_rows for a bf16 tensor [tokens][heads][head_dim] on `device`."""
     if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape and t.device == device:
         s0, s1, s2 = t.stride()
         if s2 == 1:
-            return _Rows(t.data_ptr(), s0 if shape[0] > 1 else 0, s1 if shape[1] > 1 else 0)
+            return t.data_ptr(), s0 if shape[0] > 1 else 0, s1 if shape[1] > 1 else 0
         raise ValueError(f"{name}: the channels of a head must be contiguous")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -114,6 +130,18 @@ def _rows(t: torch.Tensor, shape: tuple, device, name: str) -> _Rows:
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _rows(t: torch.Tensor, shape: tuple, device, name: str) -> _Rows:
+    return _Rows(*_strides(t, shape, device, name))
+
+
+def _out(t, shape: tuple, like: torch.Tensor, device, name: str) -> tuple:
+    """(tensor, its rows): the caller's output, checked, or a new one shaped like `like`."""
+    if t is not None:
+        return t, _byref(_rows(t, shape, device, name))
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    return t, _pack(t.data_ptr(), shape[1] * shape[2], shape[2])
 
 
 def _ints(t: torch.Tensor, shape: tuple, device, name: str) -> int:
@@ -184,17 +212,15 @@ def norm_rope(rope: Rope, q: torch.Tensor | None, k: torch.Tensor | None, positi
         if q is not None:
             hq = q.shape[1]
             shape = (n, hq, D)
-            rq = _byref(_rows(q, shape, dev, "q"))
-            q_out = q.new_empty(shape) if q_out is None else q_out
-            oq = _byref(_rows(q_out, shape, dev, "q_out"))
+            rq = _pack(*_strides(q, shape, dev, "q"))
+            q_out, oq = _out(q_out, shape, q, dev, "q_out")
         if k is not None:
             if k.dim() != 3:
                 raise ValueError("k must be [tokens][heads][head_dim]")
             hk = k.shape[1]
             shape = (n, hk, D)
-            rk = _byref(_rows(k, shape, dev, "k"))
-            k_out = k.new_empty(shape) if k_out is None else k_out
-            ok = _byref(_rows(k_out, shape, dev, "k_out"))
+            rk = _pack(*_strides(k, shape, dev, "k"))
+            k_out, ok = _out(k_out, shape, k, dev, "k_out")
         _check(_norm_rope(_byref(rope), n, hq, hk, rq, rk, _weight(q_weight, D, dev, "q_weight"),
                           _weight(k_weight, D, dev, "k_weight"), pos, oq, ok, s), "pnmix_norm_rope")
     if named is not None:
@@ -270,11 +296,10 @@ class KV4Cache:
     def append(self, batch: KV4Batch, k: torch.Tensor, v: torch.Tensor, stream=None):
         """Quantise rows k, v bf16 [n][Hkv][head_dim] (after RoPE) into the batch's places."""
         kv = (batch.n_tokens, *self._kv)
-        rk, rv = _rows(k, kv, self.device, "k"), _rows(v, kv, self.device, "v")
+        rk, rv = _pack(*_strides(k, kv, self.device, "k")), _pack(*_strides(v, kv, self.device, "v"))
         ctx, s, named = self._on(batch, stream)
         with ctx:
-            _check(_lib.pnmix_kv4_append(self._refs[0], batch.ref, _byref(rk), _byref(rv), self._refs[1], s),
-                   "pnmix_kv4_append")
+            _check(_append(self._refs[0], batch.ref, rk, rv, self._refs[1], s), "pnmix_kv4_append")
         if named is not None:
             self._used_on(named, batch, k, v)
 
@@ -284,16 +309,15 @@ class KV4Cache:
         """norm_rope of q and k and append of the rotated k and v in one pass; returns q_out."""
         n, dev = batch.n_tokens, self.device
         qs, kv = (n, *self._q), (n, *self._kv)
-        rq, rk, rv = _rows(q, qs, dev, "q"), _rows(k, kv, dev, "k"), _rows(v, kv, dev, "v")
+        rq, rk, rv = _pack(*_strides(q, qs, dev, "q")), _pack(*_strides(k, kv, dev, "k")), _pack(*_strides(v, kv, dev, "v"))
         pos = _positions(positions, rope.n_axes, n, dev)
         D = qs[2]
         wq, wk = _weight(q_weight, D, dev, "q_weight"), _weight(k_weight, D, dev, "k_weight")
         ctx, s, named = self._on(batch, stream)
         with ctx:
-            q_out = q.new_empty(qs) if q_out is None else q_out
-            _check(_lib.pnmix_kv4_append_qkv(self._refs[0], _byref(rope), batch.ref, _byref(rq), _byref(rk),
-                                             _byref(rv), wq, wk, pos, _byref(_rows(q_out, qs, dev, "q_out")),
-                                             self._refs[1], s), "pnmix_kv4_append_qkv")
+            q_out, oq = _out(q_out, qs, q, dev, "q_out")
+            _check(_append_qkv(self._refs[0], _byref(rope), batch.ref, rq, rk, rv, wq, wk, pos, oq, self._refs[1], s),
+                   "pnmix_kv4_append_qkv")
         if named is not None:
             self._used_on(named, batch, q, k, v, positions, q_weight, k_weight, q_out)
         return q_out
@@ -304,11 +328,13 @@ class KV4Cache:
         kv, dev = (batch.n_tokens, *self._kv), self.device
         ctx, s, named = self._on(batch, stream)
         with ctx:
-            k_out = torch.empty(kv, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
-            v_out = torch.empty_like(k_out) if v_out is None else v_out
-            _check(_lib.pnmix_kv4_read(self._refs[0], batch.ref, self._refs[1],
-                                       _byref(_rows(k_out, kv, dev, "k_out")),
-                                       _byref(_rows(v_out, kv, dev, "v_out")), s), "pnmix_kv4_read")
+            if k_out is None:
+                k_out = torch.empty(kv, dtype=torch.bfloat16, device=dev)
+                ok = _pack(k_out.data_ptr(), kv[1] * kv[2], kv[2])
+            else:
+                k_out, ok = _out(k_out, kv, k_out, dev, "k_out")
+            v_out, ov = _out(v_out, kv, k_out, dev, "v_out")
+            _check(_read(self._refs[0], batch.ref, self._refs[1], ok, ov, s), "pnmix_kv4_read")
         if named is not None:
             self._used_on(named, batch, k_out, v_out)
         return k_out, v_out
@@ -319,18 +345,17 @@ class KV4Cache:
         The workspace (kv4_workspace_bytes) is taken from torch's allocator for the call unless
         one is given."""
         qs, dev = (batch.n_tokens, *self._q), self.device
-        rq = _rows(q, qs, dev, "q")
+        rq = _pack(*_strides(q, qs, dev, "q"))
         ctx, s, named = self._on(batch, stream)
         with ctx:
-            out = q.new_empty(qs) if out is None else out
+            out, oo = _out(out, qs, q, dev, "out")
             if workspace is None:
                 need = _lib.pnmix_kv4_workspace_bytes(self._refs[0], batch.ref)
                 workspace = self.buffer.new_empty(max(need, 256))
             elif workspace.device != dev or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
                 raise TypeError(f"workspace must be contiguous uint8 on {dev}")
-            _check(_lib.pnmix_kv4_attention(self._refs[0], batch.ref, _byref(rq), self._refs[1],
-                                            _byref(_rows(out, qs, dev, "out")), workspace.data_ptr(),
-                                            workspace.numel(), s), "pnmix_kv4_attention")
+            _check(_attention(self._refs[0], batch.ref, rq, self._refs[1], oo, workspace.data_ptr(), workspace.numel(), s),
+                   "pnmix_kv4_attention")
         if named is not None:
             self._used_on(named, batch, q, out, workspace)
         return out
