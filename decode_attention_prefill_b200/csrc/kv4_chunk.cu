@@ -927,7 +927,7 @@ cudaError_t launch_chunk(const Geo& g, const Batch& bt, const Rows& q, const pnm
   a.out_ts = out.token_stride;
   a.out_hs = out.head_stride;
   a.wk = wk;
-  a.grain = {256, 256};
+  a.grain = {256, 128};
   a.plans = plans;
   a.rt = rt;
   return g.D == 64 ? launch_chunk_d<64>(a, ctas, s) : launch_chunk_d<128>(a, ctas, s);
