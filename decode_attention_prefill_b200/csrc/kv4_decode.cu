@@ -31,9 +31,10 @@
 //
 // Measured, the merge included: one token of 16 sequences of 32768 with 32 query and 8 KV heads
 // (head_dim 128, so half of a column tile is empty) 142 us, 4.7 TB/s or 72 % of a plain copy.  At
-// half the length 52 % of DRAM and 51 % of the integer pipe are busy at 2.4 instructions a cycle: the unpacking, two cycles an instruction,
-// runs beside the copies but does not hide behind them entirely.  Tried and not faster: the
-// blocks of a stage unrolled at four CTAs per SM (152 us), warps without work leaving early.
+// half the length 52 % of DRAM and 51 % of the integer pipe are busy at 2.4 instructions a cycle:
+// the unpacking, two cycles an instruction, runs beside the copies but does not hide behind them
+// entirely.  Tried and not faster: the blocks of a stage unrolled at four CTAs per SM (152 us),
+// warps without work leaving early.
 #include <atomic>
 
 #include "kv4_attn.cuh"

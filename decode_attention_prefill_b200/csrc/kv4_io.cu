@@ -12,7 +12,7 @@
 // shuffles and narrow stores: 123 us instead of 59 for 16384 tokens of 40 heads, and the
 // read-back, with integer conversions at a quarter of the rate, 96 us instead of 62 for
 // 2 x 32768 tokens of 8 heads.  These are 5.6 and 5.7 TB/s, 86 % of a plain copy; the write of
-// 16384 tokens of 8 + 8 heads takes 27 us, 3.3 TB/s or 50 %, and is held by its instructions.)
+// 16384 tokens of 8 + 8 heads takes 25 us, 3.5 TB/s or 54 %, and is held by its instructions.)
 // A warp's eight rows are eight tokens of a head where there are that many: their packed rows
 // lie side by side.  A token's angles (fp64 product, reduced to a turn, one sincospi per pair)
 // and its place in the cache are worked out once per CTA, while the first rows' loads are in
@@ -104,6 +104,35 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
   return d;
 }
 
+// Two fp32 lanes to an instruction, rounded like the scalar ones: the write is bound by the
+// instructions it issues (16384 tokens of 8 + 8 heads 24.8 instead of 26.7 us; in the read-back
+// they gained nothing).
+__device__ __forceinline__ uint64_t both(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 lanes_of(uint64_t a) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 // The contract's code is rint(fl(fl(x - z) / s)) clamped to [0, 15].  The correctly rounded
 // quotient comes from the correctly rounded reciprocal inv = fl(1 / s) without a division
 // (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor",
@@ -111,27 +140,29 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
 // being exact.  The rounding to a whole number is an addition of 1.5 * 2^23.  (Deciding by q
 // alone and dividing only near half-integers took longer: bf16 differences over an fp16 scale
 // are exact half-integers once in 1500 values, so half of the warps had one to divide.)
-__device__ __forceinline__ float code_sum(float x, float z, float s, float inv) {
+__device__ __forceinline__ uint64_t code_sum(uint64_t x, uint64_t minus_z, uint64_t minus_s, uint64_t inv) {
   constexpr float kMagic = 12582912.f;
-  const float d = __fsub_rn(x, z), q = __fmul_rn(d, inv);
-  return __fadd_rn(__fmaf_rn(__fmaf_rn(-q, s, d), inv, q), kMagic);      // the code in its low bits
+  const uint64_t d = add2(x, minus_z), q = mul2(d, inv);
+  return add2(fma2(fma2(q, minus_s, d), inv, q), both(kMagic, kMagic));      // the codes in the low bits
 }
 
-// Codes of eight values; `plain`: none needs the clamp.
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], uint32_t sz, float inv, bool plain) {
-  const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(sz & 0xFFFFu)));
-  const float z = __half2float(__ushort_as_half(static_cast<uint16_t>(sz >> 16)));
-  if (plain) {
-    uint32_t word = 0u - 0x4B400000u * 0x11111111u;
+// Codes of the eight values of a bf16 row piece; `plain`: none needs the clamp.
+__device__ __forceinline__ uint32_t codes_of(uint4 raw, uint32_t sz, float inv, bool plain) {
+  const float s = -__half2float(__ushort_as_half(static_cast<uint16_t>(sz & 0xFFFFu)));
+  const float z = -__half2float(__ushort_as_half(static_cast<uint16_t>(sz >> 16)));
+  const uint64_t s2 = both(s, s), z2 = both(z, z), inv2 = both(inv, inv);
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t word = plain ? 0u - 0x4B400000u * 0x11111111u : 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) word += __float_as_uint(code_sum(x[i], z, s, inv)) << (4 * i);
-    return word;
-  }
-  uint32_t word = 0u;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = __float_as_int(code_sum(x[i], z, s, inv)) - 0x4B400000;
-    word |= static_cast<uint32_t>(min(max(c, 0), 15)) << (4 * i);
+  for (int i = 0; i < 4; ++i) {
+    const float2 c = lanes_of(code_sum(both(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), z2, s2, inv2));
+    if (plain) {
+      word += __float_as_uint(c.x) << (8 * i);
+      word += __float_as_uint(c.y) << (8 * i + 4);
+    } else {
+      word |= static_cast<uint32_t>(min(max(__float_as_int(c.x) - 0x4B400000, 0), 15)) << (8 * i);
+      word |= static_cast<uint32_t>(min(max(__float_as_int(c.y) - 0x4B400000, 0), 15)) << (8 * i + 4);
+    }
   }
   return word;
 }
@@ -430,17 +461,15 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
       const float inv_own = qp.s != 0.f ? __frcp_rn(qp.s) : 0.f;      // 0 makes every code 0
       // the codes of a group lie between those of its ends, which the rounding of s and z can push
       // out of [0, 15]
-      const bool in_range = __float_as_uint(code_sum(lo, qp.z, qp.s, inv_own)) >= 0x4B400000u &&
-                            __float_as_uint(code_sum(hi, qp.z, qp.s, inv_own)) <= 0x4B40000Fu;
+      const float2 ends = lanes_of(code_sum(both(lo, hi), both(-qp.z, -qp.z), both(-qp.s, -qp.s), both(inv_own, inv_own)));
+      const bool in_range = __float_as_uint(ends.x) >= 0x4B400000u && __float_as_uint(ends.y) <= 0x4B40000Fu;
       const bool plain = __all_sync(0xffffffffu, in_range);
       uint32_t code[NG], sz[NG];
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
         sz[k] = __shfl_sync(0xffffffffu, sz_own, k, 4);
         const float inv = __shfl_sync(0xffffffffu, inv_own, k, 4);
-        float y[8];
-        unpack8(raw[k], y);
-        code[k] = codes_of(y, sz[k], inv, plain);
+        code[k] = codes_of(raw[k], sz[k], inv, plain);
       }
       if (!ROPE && rho == mine) __syncthreads();      // every thread's first row
       if (kind > 0 && place[t] >= 0) {
