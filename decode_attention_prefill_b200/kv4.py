@@ -200,6 +200,8 @@ def norm_rope(rope: Rope, q: torch.Tensor | None, k: torch.Tensor | None, positi
     """Norm of every head of q and k (where a weight is given) and rotation by position.
     q, k bf16 [n][heads][head_dim], one of them may be None; positions int32 [n_axes][n] ([n]
     with one axis).  Returns (q_out, k_out), which may be the inputs themselves."""
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
     any_ = q if q is not None else k
     if not isinstance(any_, torch.Tensor) or any_.dim() != 3:
         raise TypeError("q and k are tensors [tokens][heads][head_dim], or one of them None")
@@ -263,6 +265,8 @@ class KV4Cache:
     kv4_cache_bytes long (its contents stay); without it zeroed memory is taken."""
 
     def __init__(self, cfg: KV4Config, n_pages: int, device="cuda", buffer: torch.Tensor | None = None):
+        if not isinstance(cfg, KV4Config):
+            raise TypeError("cfg must be a KV4Config")
         cfg = KV4Config.from_buffer_copy(cfg)      # what the caller does with theirs later changes no call
         self.cfg, self.n_pages = cfg, n_pages
         nbytes = kv4_cache_bytes(cfg, n_pages)
@@ -286,6 +290,8 @@ class KV4Cache:
             _used_on(named, self.buffer)
 
     def _on(self, batch: KV4Batch, stream):
+        if not isinstance(batch, KV4Batch):
+            raise TypeError("batch must be a KV4Batch")
         if batch.device != self.device:
             raise ValueError(f"the batch is on {batch.device}, the cache on {self.device}")
         return _on(self.device, stream)
@@ -307,6 +313,8 @@ class KV4Cache:
                    positions: torch.Tensor, q_weight=None, k_weight=None, q_out: torch.Tensor | None = None,
                    stream=None) -> torch.Tensor:
         """norm_rope of q and k and append of the rotated k and v in one pass; returns q_out."""
+        if not isinstance(rope, Rope):
+            raise TypeError("rope must be a Rope")
         n, dev = batch.n_tokens, self.device
         qs, kv = (n, *self._q), (n, *self._kv)
         rq, rk, rv = _pack(*_strides(q, qs, dev, "q")), _pack(*_strides(k, kv, dev, "k")), _pack(*_strides(v, kv, dev, "v"))

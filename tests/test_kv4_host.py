@@ -182,6 +182,22 @@ def test_python_refusals():
         pm.kv4_cache_bytes(pm.KV4Config.make(8, 3), 4)
 
 
+def test_python_refuses_other_structures():
+    """The calls read what a structure's type promises, so another one is refused by type."""
+    from types import SimpleNamespace
+    cfg, x = pm.KV4Config.make(8, 2), torch.zeros(1, 1, 128, dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="Rope"):
+        pm.norm_rope(cfg, x, x, torch.zeros(1, 1, dtype=torch.int32))
+    with pytest.raises(TypeError, match="KV4Config"):
+        pm.KV4Cache(pm.Config.make(8, 2), 4)
+    c = object.__new__(pm.KV4Cache)
+    c.device, c._q, c._kv = torch.device("cuda", 0), (8, 128), (2, 128)
+    with pytest.raises(TypeError, match="Rope"):
+        c.append_qkv(None, cfg, x, x, x, None)
+    with pytest.raises(TypeError, match="KV4Batch"):
+        c._on(SimpleNamespace(device=c.device, n_tokens=1, ref=None), None)
+
+
 # ---------------------------------------------------------------- the restatement itself
 
 def test_layout_is_a_bijection_and_round_trips():
