@@ -14,9 +14,16 @@
 // 2 x 32768 tokens of 8 heads.  These are 5.6 and 5.7 TB/s, 86 % of a plain copy; the write of
 // 16384 tokens of 8 + 8 heads takes 25 us, 3.5 TB/s or 54 %, and is held by its instructions.)
 // A warp's eight rows are eight tokens of a head where there are that many: their packed rows
-// lie side by side.  A token's angles (fp64 product, reduced to a turn, one sincospi per pair)
-// and its place in the cache are worked out once per CTA, while the first rows' loads are in
-// flight; the next row's loads are issued before a row is worked on.
+// lie side by side.  A token's angles (fp64, reduced to a turn, one sincospi per pair) and its
+// place in the cache are worked out once per CTA, while the first rows' loads are in flight; the
+// next row's loads are issued before a row is worked on.
+//
+// Query rows are normed and rotated in fp32, key rows in fp64: a key is rounded to bf16 and then
+// to a 4-bit code, and neither forgives a last bit.  In fp32 one key in 21000 became the
+// neighbouring bf16, and where that key was its group's end the scale, the zero and codes of the
+// group moved by a step.  In fp64 the key is bf16(fp32(y)) of the definition's y but for a chance
+// of 2^-28 or so.  The products, sums and roundings of both are written out, so every form of the
+// kernel rounds alike and the fused write gives the bits of the separate calls.
 #include "kv4.cuh"
 #include "kv4_launch.cuh"
 
@@ -25,11 +32,12 @@ namespace kv4 {
 namespace {
 
 // Threads of a CTA; a row takes four.  Measured at the large cases (128 / 256 threads): norm and
-// rotation 59 / 66 us, write and read back 54 / 57 us with 128 threads in the read-back's kernel
+// rotation, then all in fp32, 59 / 66 us, write and read back 54 / 57 us with 128 threads in the read-back's kernel
 // too, which alone takes 66 / 61 us.
 constexpr int kInThreads = 128, kOutThreads = 256;
 constexpr int kInRows = kInThreads / 4, kOutRows = kOutThreads / 4;   // rows a CTA works on at once
 constexpr int kMaxTok = 16;                 // tokens per CTA at most
+constexpr uint32_t kOnes = 0x3F803F80u;     // 1, 1 in bf16
 
 // Sequence of packed row `row`: the last b with q_start[b] <= row, or -1 for a row outside
 // every sequence.  Called by a whole warp.
@@ -205,6 +213,22 @@ __device__ __forceinline__ void from_pieces(const uint32_t (&p)[NG], uint32_t (&
   }
 }
 
+// x c + o s: a rotated channel x of a pair whose other one is o (s negative for the pair's first).
+__device__ __forceinline__ float turned(float x, float o, float c, float s) { return __fmaf_rn(x, c, __fmul_rn(o, s)); }
+__device__ __forceinline__ double turned(double x, double o, double c, double s) {
+  return __fma_rn(x, c, __dmul_rn(o, s));
+}
+__device__ __forceinline__ void turn(float& p, float& q, float c, float s) {
+  const float p0 = p;
+  p = turned(p0, q, c, -s);
+  q = turned(q, p0, c, s);
+}
+// The pair (y, z), turned and times r.
+__device__ __forceinline__ void turn64(double y, double z, double c, double s, double r, float& p, float& q) {
+  p = static_cast<float>(__dmul_rn(turned(y, z, c, -s), r));
+  q = static_cast<float>(__dmul_rn(turned(z, y, c, s), r));
+}
+
 // How the rotation finds a channel's partner: in the same lane (pairs D / 2 apart), next to it
 // (interleaved), or through shared memory (any other distance).
 enum { kHalves = 0, kNext = 1, kAnywhere = 2 };
@@ -225,27 +249,43 @@ struct IoArgs {
   const int32_t* positions;
 };
 
-// Floats of a token's angles in shared memory: cos, sin, and a step of 16 bytes so that the
-// eight tokens of a warp meet in no bank.
+// Entries of a token's angles in shared memory: cos, sin, and a step of 16 bytes so that the
+// eight tokens of a warp meet in no bank.  In fp64 for the keys, in fp32 for the queries.
 __host__ __device__ __forceinline__ int turn_stride(int half) { return 2 * half + 4; }
+__host__ __device__ __forceinline__ int turn_stride64(int half) { return 2 * half + 2; }
+
+// cos and sin of pos * freq.  The fp64 product of a 31-bit and a 24-bit number is off by 2^-53 of
+// itself; what is left of it after n turns by Cody and Waite's reduction (2 pi in two parts, n
+// below 2^29) by 2^-51.
+__device__ __forceinline__ void turn_of(int pos, float freq, double& c, double& s) {
+  const double a = __dmul_rn(static_cast<double>(pos), static_cast<double>(freq));
+  const double n = rint(__dmul_rn(a, 0.15915494309189533577));
+  double r = __fma_rn(-n, 6.28318530717958647693, a);
+  r = __fma_rn(-n, 2.44929359829470635445e-16, r);
+  sincospi(__dmul_rn(r, 0.31830988618379067154), &s, &c);
+}
 
 // ROPE: q and k rows are normed and rotated.  QUANT: k and v rows go to the cache (otherwise
 // k rows are stored like q's).
-// CTAs per SM.  Rotating kernels: seven (72 registers) instead of the six that 80 leave room for,
-// the fused write of 3900 ragged tokens of 28 + 4 + 4 heads 22.2 against 24.2 us, the norm alone
-// the same 59.7 us; eight spill (25.1 and 64.6 us).  The plain write: eight (64 registers); ten
-// take 28.7 instead of 26.7 us.  256 channels: three, the registers that they need.
+// CTAs per SM.  Rotating kernels of 128 channels: six (80 registers; up to 32 registers' worth of
+// stores spill once a row).  At seven the fp64 of the keys spills inside: 94 instead of 66 us for the norm of 16384 tokens of 32 + 8 heads, 28.6 instead of 24.0 us
+// for the fused write of 3900 ragged tokens of 28 + 4 + 4 heads; five take 68 and 26.  (All rows in
+// fp32 at seven took 58 and 21 us.)  64 channels: seven, which is what 72 registers leave room for.
+// The plain write: eight (64 registers); ten take 28.7 instead of 26.7 us.  256 channels: three, the
+// registers that they need.
 template <int D, bool ROPE, bool QUANT, int PAIRS>
-__global__ void __launch_bounds__(kInThreads, D == 256 ? 3 : ROPE ? 7 : 8)
+__global__ void __launch_bounds__(kInThreads, D == 256 ? 3 : !ROPE ? 8 : D == 128 ? 6 : 7)
 rows_in_kernel(const __grid_constant__ IoArgs a) {
   constexpr int NG = D / 32;
-  extern __shared__ __align__(16) float shared[];   // [token][cos, sin], then [warp][8 rows][D + 4]
+  // [token][cos, sin] in fp64, the same in fp32, then [warp][8 rows][D + 4]
+  extern __shared__ __align__(16) double turns64[];
   __shared__ long long place[kMaxTok];
   __shared__ int place_tok[kMaxTok];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, w = lane & 3;
   const int ntok = 1 << a.tok_shift, tok0 = blockIdx.x << a.tok_shift;
   const int total = (a.nq + a.nk + a.nv) << a.tok_shift;   // rows of this CTA, tokens inner
   const int half = a.rope.rot_dim >> 1;
+  float* const turns32 = reinterpret_cast<float*>(turns64 + (turn_stride64(half) << a.tok_shift));
 
   // row of a lane group: kind 0 q, 1 k, 2 v; -1 none
   auto find = [&](int rho, int& t, int& head) {
@@ -290,18 +330,13 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
   if (ROPE) {
     for (int i = tid; i < half << a.tok_shift; i += kInThreads) {
       const int t = i / half, p = i - t * half;
-      float s = 0.f, c = 1.f;
-      if (tok0 + t < a.n_tokens) {
-        // angle in turns: the fp64 product of a 31-bit and a 24-bit number is off by 2^-53 of
-        // itself, 2^-31 of a turn at a million turns; reduced to [-1/2, 1/2] before it is
-        // rounded to fp32
-        const int pos = __ldg(a.positions + static_cast<size_t>(a.rope.axis[p]) * a.n_tokens + tok0 + t);
-        double turns = static_cast<double>(pos) * static_cast<double>(a.rope.inv_freq[p]) * 0.15915494309189533577;
-        turns -= rint(turns);
-        sincospif(2.f * static_cast<float>(turns), &s, &c);
-      }
-      shared[t * turn_stride(half) + p] = c;
-      shared[t * turn_stride(half) + half + p] = s;
+      double s = 0., c = 1.;
+      if (tok0 + t < a.n_tokens)
+        turn_of(__ldg(a.positions + static_cast<size_t>(a.rope.axis[p]) * a.n_tokens + tok0 + t), a.rope.inv_freq[p], c, s);
+      turns64[t * turn_stride64(half) + p] = c;
+      turns64[t * turn_stride64(half) + half + p] = s;
+      turns32[t * turn_stride(half) + p] = static_cast<float>(c);
+      turns32[t * turn_stride(half) + half + p] = static_cast<float>(s);
     }
   }
   if (ROPE) __syncthreads();      // without a rotation the places are first needed behind the codes
@@ -318,26 +353,47 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
       float x[8 * NG];
 #pragma unroll
       for (int k = 0; k < NG; ++k) unpack8(raw[k], x + 8 * k);
-      const bool turns = kind == 0 || kind == 1;
-      const uint16_t* wt = kind == 0 ? a.qw : a.kw;
-      float ss = 0.f;
+      const bool query = kind == 0, key = kind == 1;
+      const uint16_t* wt = query ? a.qw : a.kw;
+      if (__any_sync(0xffffffffu, query)) {
+        float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8 * NG; ++i) ss = fmaf(x[i], x[i], ss);
-      ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-      ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-      if (wt && turns) {
-        const float r = rsqrtf(ss * (1.0f / D) + a.rope.eps);
+        for (int i = 0; i < 8 * NG; ++i) ss = __fmaf_rn(x[i], x[i], ss);
+        ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, 1));
+        ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, 2));
+        if (query && wt) {
+          const float r = rsqrtf(__fmaf_rn(ss, 1.0f / D, a.rope.eps));
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-          float wf[8];
-          unpack8(__ldg(reinterpret_cast<const uint4*>(wt) + 4 * k + w), wf);
+          for (int k = 0; k < NG; ++k) {
+            float wf[8];
+            unpack8(__ldg(reinterpret_cast<const uint4*>(wt) + 4 * k + w), wf);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[8 * k + i] *= r * wf[i];
+            for (int i = 0; i < 8; ++i) x[8 * k + i] = __fmul_rn(x[8 * k + i], __fmul_rn(r, wf[i]));
+          }
         }
       }
-      const float* cs = shared + t * turn_stride(half);
+      double r64 = 1.;
+      if (__any_sync(0xffffffffu, key) && a.kw) {
+        double ss = 0.;
+#pragma unroll
+        for (int i = 0; i < 8 * NG; ++i) ss = __fma_rn(static_cast<double>(x[i]), static_cast<double>(x[i]), ss);
+        ss = __dadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, 1));
+        ss = __dadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, 2));
+        r64 = rsqrt(__fma_rn(ss, 1.0 / D, static_cast<double>(a.rope.eps)));
+      }
+      // a channel of the key row times its weight (the i-th of the octet's bf16 weights g): exact in
+      // fp32, as both have eight bits, inside its range.  The norm's factor is left for the end.
+      auto weighted = [&](float v, const uint4& g, int i) {
+        const uint32_t pair = i < 2 ? g.x : i < 4 ? g.y : i < 6 ? g.z : g.w;
+        return static_cast<double>(__fmul_rn(v, __uint_as_float((i & 1) ? pair & 0xFFFF0000u : pair << 16)));
+      };
+      auto weights = [&](int ch) {
+        return wt ? __ldg(reinterpret_cast<const uint4*>(wt + ch)) : make_uint4(kOnes, kOnes, kOnes, kOnes);
+      };
+      const float* cs = turns32 + t * turn_stride(half);
+      const double* cs64 = turns64 + t * turn_stride64(half);
       if constexpr (PAIRS == kHalves) {
-        if (turns) {
+        if (query) {
 #pragma unroll
           for (int k = 0; k < NG / 2; ++k) {
             float c[8], s[8];
@@ -347,32 +403,52 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
               *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(cs + half + 32 * k + 8 * w + i);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float &p = x[8 * k + i], &q = x[8 * (k + NG / 2) + i];
-              const float p0 = p;
-              p = p0 * c[i] - q * s[i];
-              q = q * c[i] + p0 * s[i];
+            for (int i = 0; i < 8; ++i) turn(x[8 * k + i], x[8 * (k + NG / 2) + i], c[i], s[i]);
+          }
+        } else if (key) {
+#pragma unroll
+          for (int k = 0; k < NG / 2; ++k) {
+            const int ch = 32 * k + 8 * w;
+            const uint4 g = weights(ch), h = weights(ch + D / 2);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const double2 c = *reinterpret_cast<const double2*>(cs64 + ch + i);
+              const double2 s = *reinterpret_cast<const double2*>(cs64 + half + ch + i);
+              float &p0 = x[8 * k + i], &q0 = x[8 * (k + NG / 2) + i];
+              float &p1 = x[8 * k + i + 1], &q1 = x[8 * (k + NG / 2) + i + 1];
+              turn64(weighted(p0, g, i), weighted(q0, h, i), c.x, s.x, r64, p0, q0);
+              turn64(weighted(p1, g, i + 1), weighted(q1, h, i + 1), c.y, s.y, r64, p1, q1);
             }
           }
         }
       } else if constexpr (PAIRS == kNext) {
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-          if (turns && 32 * k + 8 * w < a.rope.rot_dim) {
+          const bool turns = 32 * k + 8 * w < a.rope.rot_dim;
+          if (query && turns) {
             float c[4], s[4];
             *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(cs + 16 * k + 4 * w);
             *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(cs + half + 16 * k + 4 * w);
 #pragma unroll
+            for (int i = 0; i < 4; ++i) turn(x[8 * k + 2 * i], x[8 * k + 2 * i + 1], c[i], s[i]);
+          } else if (key) {
+            const uint4 g = weights(32 * k + 8 * w);
+#pragma unroll
             for (int i = 0; i < 4; ++i) {
+              const int pair = 16 * k + 4 * w + i;
               float &p = x[8 * k + 2 * i], &q = x[8 * k + 2 * i + 1];
-              const float p0 = p;
-              p = p0 * c[i] - q * s[i];
-              q = q * c[i] + p0 * s[i];
+              const double y = weighted(p, g, 2 * i), z = weighted(q, g, 2 * i + 1);
+              if (turns) {
+                turn64(y, z, cs64[pair], cs64[half + pair], r64, p, q);
+              } else {
+                p = static_cast<float>(__dmul_rn(y, r64));
+                q = static_cast<float>(__dmul_rn(z, r64));
+              }
             }
           }
         }
       } else {
-        float* row = shared + (turn_stride(half) << a.tok_shift) + (warp * 8 + (lane >> 2)) * (D + 4);
+        float* row = turns32 + (turn_stride(half) << a.tok_shift) + (warp * 8 + (lane >> 2)) * (D + 4);
         __syncwarp();   // the rows before were read
 #pragma unroll
         for (int i = 0; i < 8 * NG; i += 4)
@@ -381,21 +457,31 @@ rows_in_kernel(const __grid_constant__ IoArgs a) {
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
           const int ch = 32 * k + 8 * w;
-          if (turns && ch < a.rope.rot_dim) {
-            const bool first = ch < half;
-            const int p = first ? ch : ch - half;
-            const float* other = row + (first ? ch + half : ch - half);
+          const bool turns = ch < a.rope.rot_dim, first = ch < half;
+          const int p = first ? ch : ch - half, to = first ? ch + half : ch - half;    // the pair, the partner channel
+          if (query && turns) {
 #pragma unroll
             for (int i = 0; i < 8; i += 4) {
-              const float4 o = *reinterpret_cast<const float4*>(other + i);
+              const float4 o = *reinterpret_cast<const float4*>(row + to + i);
               const float4 c = *reinterpret_cast<const float4*>(cs + p + i);
               float4 s = *reinterpret_cast<const float4*>(cs + half + p + i);
               if (first) s = make_float4(-s.x, -s.y, -s.z, -s.w);
               float* y = x + 8 * k + i;
-              y[0] = y[0] * c.x + o.x * s.x;
-              y[1] = y[1] * c.y + o.y * s.y;
-              y[2] = y[2] * c.z + o.z * s.z;
-              y[3] = y[3] * c.w + o.w * s.w;
+              y[0] = turned(y[0], o.x, c.x, s.x);
+              y[1] = turned(y[1], o.y, c.y, s.y);
+              y[2] = turned(y[2], o.z, c.z, s.z);
+              y[3] = turned(y[3], o.w, c.w, s.w);
+            }
+          } else if (key) {
+            const uint4 g = weights(ch), h = turns ? weights(to) : g;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              double y = weighted(x[8 * k + i], g, i);
+              if (turns) {
+                const double s = cs64[half + p + i];
+                y = turned(y, weighted(row[to + i], h, i), cs64[p + i], first ? -s : s);
+              }
+              x[8 * k + i] = static_cast<float>(__dmul_rn(y, r64));
             }
           }
         }
@@ -571,7 +657,7 @@ rows_out_kernel(const __grid_constant__ OutArgs a) {
 
 // Tokens per CTA at most (log2; neighbours in the cache are written by one warp), fewer while
 // the grid would not fill the GPU.  Measured at 16384 tokens with 1, 2, 4 and 8 tokens: norm and
-// rotation of 40 heads -, 59, 61 and 72 us; the write of 16 rows a token (and its read-back) -,
+// rotation of 40 heads, then all in fp32, -, 59, 61 and 72 us; the write of 16 rows a token (and its read-back) -,
 // 55, 54 and 55 us.
 int token_shift(int n_tokens, int most) {
   int s = most;
@@ -582,10 +668,12 @@ int token_shift(int n_tokens, int most) {
 template <int D, bool ROPE, bool QUANT, int PAIRS>
 cudaError_t launch_pairs(const IoArgs& a, cudaStream_t s) {
   const int ctas = (a.n_tokens + (1 << a.tok_shift) - 1) >> a.tok_shift;
-  size_t floats = 0;
-  if (ROPE) floats += static_cast<size_t>(turn_stride(a.rope.rot_dim >> 1)) << a.tok_shift;
-  if (ROPE && PAIRS == kAnywhere) floats += kInRows * (D + 4);
-  rows_in_kernel<D, ROPE, QUANT, PAIRS><<<ctas, kInThreads, floats * sizeof(float), s>>>(a);
+  const int half = a.rope.rot_dim >> 1;
+  size_t bytes = 0;
+  if (ROPE)
+    bytes += (turn_stride64(half) * sizeof(double) + turn_stride(half) * sizeof(float)) << a.tok_shift;
+  if (ROPE && PAIRS == kAnywhere) bytes += kInRows * (D + 4) * sizeof(float);
+  rows_in_kernel<D, ROPE, QUANT, PAIRS><<<ctas, kInThreads, bytes, s>>>(a);
   return cudaGetLastError();
 }
 

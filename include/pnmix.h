@@ -636,8 +636,9 @@ typedef struct {
  * Norm of every query and key head and rotation by position, in one pass:
  *     y = x / sqrt(mean(x^2) + eps) * weight   (weight bf16 [head_dim]; NULL: y = x),
  *     then every pair (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin),
- * in fp32 (angles in fp64, reduced to a turn before they are rounded, so far positions keep
- * their angle), rounded to bf16 once.  n_tokens rows (0 allowed: nothing is done); q and
+ * queries in fp32 and rounded to bf16 once (angles in fp64, so far positions keep theirs); keys, of
+ * which a cache stores 4-bit codes, in fp64 (x * weight in fp32, where it is exact), rounded to fp32
+ * and then to bf16.  n_tokens rows (0 allowed: nothing is done); q and
  * q_out have n_q_heads heads, k and k_out n_k_heads; either head count may be 0, and its
  * pointers are then not looked at.  positions: int32 [n_axes][n_tokens], any values.
  * An output may be its own input (same pointer and strides), otherwise it overlaps none.

@@ -1,0 +1,82 @@
+"""What the operators of the 4-bit paged cache promise about roundings and ranges, on the GPU."""
+import numpy as np
+import pytest
+import torch
+
+import kv4_ref as ref
+from test_kv4 import DEV, Setup, axes_of, dev, host, pm, rows  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# D, rotated channels, interleaved: pairs half a head apart, neighbours, any other distance
+FORMS = [(128, 128, False), (128, 128, True), (128, 96, False), (128, 48, True), (64, 64, False), (64, 64, True),
+         (64, 32, False), (128, 0, False)]
+
+
+def rope_of(pm, D, rot, inter, axes):  # noqa: F811
+    inv = [np.float32(500000.0 ** (-2 * i / max(rot, 1))) for i in range(rot // 2)]
+    args = dict(inv_freq=inv, axis=axes_of(rot, axes), rot=rot, interleaved=inter, eps=2.0 ** -20)
+    rope = pm.Rope.make(D, rot, inv_freq=inv, axes=args["axis"], interleaved=inter, eps=args["eps"])
+    rope.n_axes = axes
+    return rope, args
+
+
+@pytest.mark.parametrize("D,rot,inter", FORMS)
+@pytest.mark.parametrize("weights", [True, False])
+def test_keys_are_the_64_bit_definitions(pm, D, rot, inter, weights):  # noqa: F811
+    """Rotated keys are bf16(fp32(y)) of the definition's y, and what the fused write stores are the
+    codes of those rows.  The kernel's y is off by some 2^-50; it rounds otherwise than the
+    definition's only where that spans a border of fp32 next to one of bf16, 2^-42 a key.  (fp32
+    arithmetic moves one key in 20000 to the neighbouring bf16.)"""
+    Hq, Hkv, n, page, axes = 4, 4, 4000, 64, 3
+    q, k, v = (rows(i, n, h, D) for i, h in ((1, Hq), (2, Hkv), (3, Hkv)))
+    r = np.random.default_rng(4)
+    w = [ref.bf16(1 + 0.3 * r.standard_normal(D)) if weights else None for _ in range(2)]
+    wd = [None if x is None else dev(x) for x in w]
+    pos = r.integers(0, 200000, (axes, n)).astype(np.int32)
+    rope, args = rope_of(pm, D, rot, inter, axes)
+    y, _ = ref.norm_rope(k, w[1], pos, **args)
+    want = ref.bf16_from_f32(y.astype(np.float32))
+    got = host(pm.norm_rope(rope, dev(q), dev(k), dev(pos, torch.int32), *wd)[1])
+    assert np.array_equal(got, want), (got != want).sum()
+    s = Setup(pm, [n], [n], Hq, Hkv, D, page)
+    s.cache.append_qkv(s.batch, rope, dev(q), dev(k), dev(v), dev(pos, torch.int32), *wd)
+    ko, vo = s.cache.read(s.batch)
+    assert np.array_equal(host(ko), ref.bf16_from_f32(ref.stand_for(*ref.quantise(want))))
+    assert np.array_equal(host(vo), ref.bf16_from_f32(ref.stand_for(*ref.quantise(v))))
+
+
+@pytest.mark.parametrize("D,rot,inter", FORMS)
+@pytest.mark.parametrize("weights", [True, False])
+@pytest.mark.parametrize("T,Hq,Hkv", [([1], 4, 2), ([40, 1, 300], 7, 1), ([1400, 0, 9], 6, 3)])
+def test_every_form_of_the_fused_write_equals_the_two_calls(pm, D, rot, inter, weights, T, Hq, Hkv):  # noqa: F811
+    a, b = (Setup(pm, [t + 5 for t in T], T, Hq, Hkv, D, 32) for _ in range(2))
+    qkv = dev(rows(21, a.n, Hq + 2 * Hkv, D))
+    q, k, v = qkv.split([Hq, Hkv, Hkv], 1)
+    rope, _ = rope_of(pm, D, rot, inter, 2)
+    pos = dev(np.random.default_rng(22).integers(-50, 70000, (2, a.n)).astype(np.int32), torch.int32)
+    w = [dev(ref.bf16(1 + 0.2 * np.random.default_rng(i).standard_normal(D))) if weights else None for i in range(2)]
+    qo = a.cache.append_qkv(a.batch, rope, q, k, v, pos, *w)
+    q2, k2 = pm.norm_rope(rope, q, k, pos, *w)
+    b.cache.append(b.batch, k2, v)
+    assert torch.equal(qo, q2) and torch.equal(a.cache.pages(), b.cache.pages())
+
+
+def test_keys_of_extreme_rows(pm):  # noqa: F811
+    """Rows whose squares leave fp32, zeros, infinities and NaN: as the definition has them."""
+    D, n = 128, 7
+    k = rows(31, n, 1, D)
+    k[1] *= np.float32(1e30)
+    k[2] = ref.bf16(k[2].astype(np.float64) * 1e-36)
+    k[3] = 0
+    k[4, 0, 5], k[5, 0, 6] = np.inf, np.nan
+    k = host(dev(k))        # what the call sees: bf16
+    w = ref.bf16(1 + 0.3 * np.random.default_rng(32).standard_normal(D))
+    pos = np.zeros((1, n), np.int32)
+    rope, args = rope_of(pm, D, D, False, 1)
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = ref.bf16_from_f32(ref.norm_rope(k, w, pos, **args)[0].astype(np.float32))
+    got = host(pm.norm_rope(rope, None, dev(k), dev(pos[0], torch.int32), None, dev(w))[1])
+    keep = [0, 1, 2, 3, 6]
+    assert np.array_equal(got[keep], want[keep])
+    assert np.isnan(got[4, 0, 5]) and np.isnan(got[5]).all()
