@@ -22,8 +22,9 @@
 //   softmax     one pass over S in TMEM, 32 columns at a time: p = 2^(x - m), summed in fp32
 //               and rounded to fp16 (2^-11 of each weight at most) over the S it came from.  The
 //               reference m moves only when a row's sum of 32 passes 2^15 (so no p is above the
-//               fp16 range, and no maximum has to be taken otherwise); what the row has so far,
-//               in TMEM and out of it, is then rescaled by a power of two
+//               fp16 range, and no maximum has to be taken otherwise), once for these 32 at most:
+//               behind it their sum is in range by construction (kv4_softmax.cuh).  What the row
+//               has so far, in TMEM and out of it, is then rescaled
 //   O += P V    A = P from TMEM, B = value tile
 // What every role runs once per piece is kept short: straight-line code that is met cold costs
 // about ten cycles an instruction here (five roles share the instruction cache), and a spilled
@@ -46,6 +47,7 @@
 
 #include "kv4_attn.cuh"
 #include "kv4_launch.cuh"
+#include "kv4_softmax.cuh"
 
 namespace pnmix {
 namespace kv4 {
@@ -200,7 +202,8 @@ struct Smem {
   static constexpr int kQ = kV + 2 * kTileBytes;            // [128 rows][D], two in the two-tile form
   static constexpr int kHalfBytes = 4 * 20 * D;             // 4 blocks
   static constexpr int kMl = 0;                             // after the ring: [128][2], stream 1's m, l
-  static constexpr int kBars = kMl + 128 * 8;
+  static constexpr int kBase = kMl + 128 * 8;               // [2][128] base of a stream's row (kv4_softmax.cuh)
+  static constexpr int kBars = kBase + 2 * 128 * 4;
   static constexpr int kJobs = kBars + 384;                 // two pieces of work
   static constexpr int kSlots = kJobs + 96;                 // the partition's place in its work
   static constexpr int kEnd = kSlots + 64;
@@ -433,7 +436,10 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
         if (stream == 1) fac = ml[0];
       }
 
-      float ref = -1e30f, den = 0.f;    // lower than any logit: the first one moves it
+      float ref = kFirstReference, den = 0.f;
+      bool far = false;                 // a row of the warp has a base other than 0
+      float* const base = reinterpret_cast<float*>(rest + S::kBase) + tid;      // out of the registers
+      *base = 0.f;
       int mine = 0;                     // tiles of this stream so far
       int lim = seen - (jb.lo + (dual ? 0 : stream)) * kTile;     // columns of the tile below it are visible
       for (int i = dual ? 0 : stream; i < nt; i += dual ? 1 : 2, lim -= dual ? kTile : 2 * kTile) {
@@ -463,17 +469,36 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
           d0 = add2(d0, d1.x, d1.y);
           return d0.x + d0.y;
         };
-        // The weights of 32 columns stay in registers until their sum is found to be in range, so
-        // their logits can still be read again.
+        for (int c = 0; c < 4;) {
+          float sum = 0.f;
+          // The weights of 32 columns stay in registers until their sum is found to be in range, so
+          // their logits can still be read again.
+          if (!far) {
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+            for (; c < 4; ++c) {
+              uint32_t cur[32], p[16];
+              tmem_ld32_start(t_s + 32 * c, cur);
+              tmem_ld_wait(cur);
+              sum = weights(32 * c, cur, p);
+              if (__any_sync(0xffffffffu, sum > kTop)) break;
+              den += sum;
+              tmem_st16(t_s + 16 * c, p);     // over columns that were read
+            }
+            if (c == 4) break;
+          }
+          // Out of range, or rows with a base: 32 columns with a move of the reference, one at most (the
+          // commit of these logits covers the stream's earlier value products, so O is idle).
           uint32_t cur[32], p[16];
-          tmem_ld32_start(t_s + 32 * c, cur);
-          tmem_ld_wait(cur);
-          float sum = weights(32 * c, cur, p);
-          while (__any_sync(0xffffffffu, sum > kTop)) {
-            // the reference of some row moves up (the commit of these logits covers the stream's
-            // earlier value products, so O is idle)
+          for (bool known = !far, moved = false;; known = false, moved = true) {
+            if (!known) {
+              tmem_ld32_start(t_s + 32 * c, cur);
+              tmem_ld_wait(cur);
+              const float b = *base;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) cur[k] = __float_as_uint(__uint_as_float(cur[k]) - b);
+              sum = weights(32 * c, cur, p);
+              if (moved || !__any_sync(0xffffffffu, sum > kTop)) break;
+            }
             uint32_t y[16];
             float mx = -INFINITY;
 #pragma unroll 1
@@ -485,11 +510,13 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
             }
             float f = 1.f;
             if (sum > kTop) {      // some weight is 2^10 at least
-              const float to = ceilf(mx * fac);
-              f = ex2(ref - to);
-              ref = to;
+              const RowRef from = {*base, ref}, to = move_reference(from, mx, fac);
+              f = ex2(move_exponent(from, to, fac));
+              *base = to.base;
+              ref = to.ref;
               den *= f;
             }
+            far = __any_sync(0xffffffffu, *base != 0.f);
             if (mine > 0) {
 #pragma unroll 1
               for (int k = 0; k < D; k += 16) {
@@ -500,20 +527,20 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
               }
             }
             tmem_wait_st();
-            const __half2 f2 = __float2half2_rn(f);
 #pragma unroll 1
             for (int k = 0; k < 16 * c; k += 16) {     // this tile's weights that are written already
               tmem_ld16(t_s + k, y);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = as_u32(__hmul2(as_h2(y[e]), f2));
+              for (int e = 0; e < 16; ++e) {
+                const float2 w = __half22float2(as_h2(y[e]));
+                y[e] = pack_f16x2(w.x * f, w.y * f);
+              }
               tmem_st16(t_s + k, y);
             }
-            tmem_ld32_start(t_s + 32 * c, cur);
-            tmem_ld_wait(cur);
-            sum = weights(32 * c, cur, p);
           }
           den += sum;
-          tmem_st16(t_s + 16 * c, p);     // over columns that were read
+          tmem_st16(t_s + 16 * c, p);
+          ++c;
         }
         tmem_wait_st();
         tc_fence_before();
@@ -524,10 +551,10 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
       // ---- the stream's last product
       if (ok && mine > 0) ok = wait(o_done + stream, no++, kCommitLimit);
       tc_fence_after();
-      float w0 = 1.f, w1 = 0.f;
+      float w0 = 1.f, w1 = 0.f, top = reference_of({*base, ref}, fac);
       if (!dual) {        // join the streams: stream 0's threads read both rows of O
         if (stream == 1) {
-          ml[0] = ref;
+          ml[0] = top;
           ml[1] = den;
         }
         tc_fence_before();
@@ -535,11 +562,11 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
         tc_fence_after();
         if (stream == 0) {
           const float m1 = ml[0], l1 = ml[1];
-          const float m = l1 == 0.f ? ref : den == 0.f ? m1 : fmaxf(ref, m1);
-          w0 = den == 0.f ? 0.f : ex2(ref - m);
+          const float m = l1 == 0.f ? top : den == 0.f ? m1 : fmaxf(top, m1);
+          w0 = den == 0.f ? 0.f : ex2(top - m);
           w1 = l1 == 0.f ? 0.f : ex2(m1 - m);
           den = (den == 0.f ? 0.f : den * w0) + (l1 == 0.f ? 0.f : l1 * w1);
-          ref = m;
+          top = m;
         }
       }
       if (dual || stream == 0) {
@@ -547,7 +574,7 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
         const bool has0 = mine > 0, has1 = !dual && nt > 1;
         const float inv = den == 0.f ? 0.f : 1.f / den;
         float* part = part_of<D>(a.wk.part, slot, a.rt);
-        if (slot >= 0 && live) reinterpret_cast<float2*>(part)[v] = make_float2(ref, den);
+        if (slot >= 0 && live) reinterpret_cast<float2*>(part)[v] = make_float2(top, den);
         // the stream's logits are done, so its query tile is free to turn the rows around in
         uint8_t* turn = qa + (warp & 3) * (64 * D);
 #pragma unroll 1

@@ -1,0 +1,45 @@
+// kv4_softmax.cuh -- where a row's softmax reference stands in the attention over the 4-bit paged
+// cache, and how it moves.  Plain arithmetic that compiles for the host too, where it is tested.
+#pragma once
+
+#include <math.h>
+
+#ifdef __CUDACC__
+#define PNMIX_BOTH __host__ __device__ __forceinline__
+#else
+#define PNMIX_BOTH inline
+#endif
+
+namespace pnmix {
+namespace kv4 {
+
+// A weight of a raw logit x of a row with factor fac (to the log2 domain) is 2^e with
+// e = fl((x - base) fac - ref), one fma behind the difference.  base is 0 while the scaled logits are
+// moderate: then fl(mx fac) is within 2^-5 of the largest one, so a reference made from it bounds
+// the weights.  From 2^20 on the spacing of fp32 makes such a reference useless (at 2^28 it is 32,
+// and e may be 16 for the maximum itself), so the row's largest raw logit is taken away first: e is
+// then at most -ref by its sign alone, whatever the size of the logits.
+constexpr float kFarLogit = 1048576.f;
+constexpr float kFirstReference = -1e30f;   // lower than any logit: the first one moves it
+
+struct RowRef {
+  float base, ref;
+};
+
+// The reference after a move to the largest raw logit mx: no weight is above 2^(2^-5).
+PNMIX_BOTH RowRef move_reference(const RowRef& old, float mx, float fac) {
+  const float t = mx * fac;
+  if (old.base == 0.f && fabsf(t) < kFarLogit) return {0.f, ceilf(t)};
+  return {mx, 0.f};
+}
+
+// log2 of what the row's sums so far are multiplied by in that move.
+PNMIX_BOTH float move_exponent(const RowRef& old, const RowRef& now, float fac) {
+  return fmaf(old.base - now.base, fac, old.ref - now.ref);
+}
+
+// The reference in the log2 domain, for joining partial sums of a row.
+PNMIX_BOTH float reference_of(const RowRef& r, float fac) { return fmaf(r.base, fac, r.ref); }
+
+}  // namespace kv4
+}  // namespace pnmix

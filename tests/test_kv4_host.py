@@ -239,3 +239,89 @@ def test_bf16_rounding_of_the_restatement():
     assert (got != want).sum() <= 2
     f = x.astype(np.float32)
     assert np.array_equal(ref.bf16_from_f32(f), torch.from_numpy(f).to(torch.bfloat16).float().numpy())
+
+
+# ---------------------------------------------------------------- the reference of a row's softmax
+
+def compiled(tmp_path, body):
+    """A C++ function over the arithmetic that the kernels share with the host."""
+    import os
+    import subprocess
+    csrc = os.path.join(os.path.dirname(os.path.abspath(pm.__file__)), "csrc")
+    src, so = tmp_path / "t.cpp", tmp_path / "t.so"
+    src.write_text('#include "kv4_softmax.cuh"\nusing namespace pnmix::kv4;\n' + body)
+    subprocess.run(["g++", "-O1", "-ffp-contract=off", "-std=c++17", "-shared", "-fPIC", "-I", csrc, str(src), "-o",
+                    str(so)], check=True)
+    return ctypes.CDLL(str(so))
+
+
+COLUMNS = """
+// Rows of n columns in steps of 32, as the many-row kernel takes them: weights, one move where a
+// step's sum passes 2^15, the weights again.  Gives for each row the largest sum of a step behind
+// its move, and the weights in the end, relative to the last reference.
+extern "C" void rows32(const float* x, const float* fac, int rows, int n, float* worst, double* weight) {
+  for (int r = 0; r < rows; ++r) {
+    RowRef ref = {0.f, kFirstReference};
+    worst[r] = 0.f;
+    for (int c = 0; c < n; c += 32) {
+      const float* at = x + (long)r * n + c;
+      for (int turn = 0; turn < 2; ++turn) {
+        float sum = 0.f, mx = -INFINITY;
+        for (int k = 0; k < 32; ++k) {
+          const float p = exp2f(fmaf(at[k] - ref.base, fac[r], -ref.ref));
+          weight[(long)r * n + c + k] = p;
+          sum += p;
+          mx = fmaxf(mx, at[k]);
+        }
+        if (turn == 1 || !(sum > 32768.f)) {
+          worst[r] = fmaxf(worst[r], sum);
+          break;
+        }
+        const RowRef to = move_reference(ref, mx, fac[r]);
+        const double f = exp2(move_exponent(ref, to, fac[r]));
+        for (int k = 0; k < c; ++k) weight[(long)r * n + k] *= f;
+        ref = to;
+      }
+    }
+  }
+}
+"""
+
+
+def run_rows(tmp_path, x, fac):
+    lib = compiled(tmp_path, COLUMNS)
+    x, fac = np.ascontiguousarray(x, np.float32), np.ascontiguousarray(fac, np.float32)
+    worst, w = np.zeros(len(x), np.float32), np.zeros(x.shape, np.float64)
+    P_ = lambda a: a.ctypes.data_as(ctypes.c_void_p)  # noqa: E731
+    lib.rows32(P_(x), P_(fac), ctypes.c_int(x.shape[0]), ctypes.c_int(x.shape[1]), P_(worst), P_(w))
+    return worst, w
+
+
+@pytest.mark.parametrize("log2", range(-10, 96, 5))
+def test_one_move_of_the_reference_is_enough(tmp_path, log2):
+    """Logits of any size up to 2^95: behind one move the 32 weights stay in range (a second move
+    would change nothing), and the largest weight of the row does not vanish."""
+    r = np.random.default_rng(300 + log2)
+    rows_, n = 4000, 96
+    fac = (1 + r.random(rows_)) * 2.0 ** r.integers(-20, 20, rows_)
+    size = 2.0 ** log2 * (1 + r.random(rows_))
+    x = r.standard_normal((rows_, n)) * r.choice([1, 1e-3, 1e-7], (rows_, 1)) + r.choice([-1, 0, 1], (rows_, 1))
+    x = (x * (size / fac)[:, None]).astype(np.float32)
+    worst, w = run_rows(tmp_path, x, fac)
+    # 32 weights of at most 2^(2^-5) each where the row moved, else what was in range anyway
+    assert np.isfinite(w).all() and (worst <= 32768).all()
+    top = np.take_along_axis(w, x.argmax(1)[:, None], 1)[:, 0]
+    assert (top >= 2.0 ** -1).all() and (w <= top[:, None] * (1 + 2.0 ** -20)).all()
+
+
+def test_weights_of_moderate_logits_are_the_softmax(tmp_path):
+    r = np.random.default_rng(41)
+    x = (r.standard_normal((500, 192)) * r.uniform(0.1, 200, (500, 1))).astype(np.float32)
+    fac = r.uniform(0.01, 2, 500).astype(np.float32)
+    _, w = run_rows(tmp_path, x, fac)
+    z = x.astype(np.float64) * fac[:, None].astype(np.float64)
+    want = 2.0 ** (z - z.max(1, keepdims=True))
+    want /= want.sum(1, keepdims=True)
+    got = w / w.sum(1, keepdims=True)
+    # exponents of up to 2^11 are off by 2^-14 of a bit at most, exp2f by a few 2^-24
+    assert (np.abs(got - want) <= want * 2.0 ** -12 + 1e-30).all()

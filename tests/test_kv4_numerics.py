@@ -80,3 +80,62 @@ def test_keys_of_extreme_rows(pm):  # noqa: F811
     keep = [0, 1, 2, 3, 6]
     assert np.array_equal(got[keep], want[keep])
     assert np.isnan(got[4, 0, 5]) and np.isnan(got[5]).all()
+
+
+# ---------------------------------------------------------------- the range of logits
+
+def cached(pm, kv_len, T, Hq, Hkv, D, k, v, page=32):  # noqa: F811
+    """A batch over sequences that all hold the rows k, v [tokens][Hkv][D]."""
+    s = Setup(pm, kv_len, T, Hq, Hkv, D, page)
+    for b, n in enumerate(kv_len):
+        one = pm.KV4Batch(dev(np.array([n]), torch.int32), dev(s.table[b:b + 1], torch.int32), n_tokens=n)
+        s.cache.append(one, dev(k[:n]), dev(v[:n]))
+    return s
+
+
+def mean_of_tokens(v, tokens):
+    """What attention gives whose weight lies evenly on some tokens, and what may be off: the values'
+    fp16 form (2^-11 of code * s and of the zero point), the weights' (2^-11 each) and bf16."""
+    x = ref.stand_for(*ref.quantise(v[tokens])).astype(np.float64)
+    return x.mean(0), np.abs(x).mean(0) * (2.0 ** -8 + 2.0 ** -10) + np.abs(v[tokens]).max() * 2.0 ** -10
+
+
+FAR = [1e4, 1e6, 1e9, 1e20, 1e29]
+
+
+@pytest.mark.parametrize("T", [20, 140])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("amp", FAR)
+def test_attention_where_logits_are_very_large(pm, T, D, amp):  # noqa: F811
+    """Three equal tokens, in three tiles, whose logit is far above all others: each row is their mean."""
+    r = np.random.default_rng(401)
+    n = 600
+    k, v = r.standard_normal((n, 1, D)) * 0.05, rows(402, n, 1, D)
+    base = ref.bf16(np.sign(r.standard_normal(D)) * (1 + r.random(D)))
+    k = ref.bf16(k)
+    hot = [3, 200, 300]
+    k[hot] = base
+    s = cached(pm, [n], [T], 4, 1, D, k, v)
+    q = ref.bf16(np.tile(base, (T, 4, 1)) * amp)
+    out = host(s.cache.attend(s.batch, dev(q)))
+    assert s.cache.read_error() == 0
+    want, tol = mean_of_tokens(v, hot)
+    assert (np.abs(out - want) <= tol).all(), np.abs(out - want).max()
+
+
+@pytest.mark.parametrize("T", [40, 140])
+@pytest.mark.parametrize("amp", FAR)
+def test_attention_where_very_large_logits_grow(pm, T, amp):  # noqa: F811
+    """Each token's logit is a twentieth above the one's before, so every row is its own token's value."""
+    r = np.random.default_rng(403)
+    n, D = 150, 128
+    base = ref.bf16(r.standard_normal(D))
+    k = ref.bf16(1.05 ** np.arange(n)[:, None, None] * base * 0.05)
+    v = rows(404, n, 1, D)
+    s = cached(pm, [n], [T], 2, 1, D, k, v)
+    q = ref.bf16(np.tile(base, (T, 2, 1)) * amp)
+    out = host(s.cache.attend(s.batch, dev(q)))
+    assert s.cache.read_error() == 0
+    for j in range(T):
+        want, tol = mean_of_tokens(v, [n - T + j])
+        assert (np.abs(out[j] - want) <= tol).all(), (j, np.abs(out[j] - want).max())
