@@ -17,8 +17,8 @@
 //            as s * sum + z * (sum of the query's channels of that group), both fp32.
 //   softmax  p = 2^(x - m'), x the scaled logit in the log2 domain; the reference m' of a row
 //            is moved only when p times the token's largest value scale would pass 2^15 (then to
-//            2^8), so p * s stays inside fp16 whatever the size of the values, and the
-//            accumulators are rescaled a few times per run.
+//            2^8), so p * s stays inside fp16 whatever the size of the values and logits
+//            (kv4_softmax.cuh), and the accumulators are rescaled a few times per run.
 //   values   A = value codes, 16 channels x 16 tokens; two tokens' words are joined by a byte
 //            permute and masked like the keys.  B = p * s_v per channel group, rounded once to
 //            fp16 (2^-11 of each weight at most) and transposed by movmatrix from the logits'
@@ -39,6 +39,7 @@
 
 #include "kv4_attn.cuh"
 #include "kv4_launch.cuh"
+#include "kv4_softmax.cuh"
 
 namespace pnmix {
 namespace kv4 {
@@ -102,6 +103,7 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
   __shared__ uint64_t bars[kWarps][kStages];
   __shared__ long long tmp[2 * kWarps];
   __shared__ PieceSlot slots[kWarps];
+  __shared__ float bases[kWarps][RT];      // of the warp's rows (kv4_softmax.cuh)
   uint64_t* full = bars[warp];
   if (lane == 0) {
     for (int k = 0; k < kStages; ++k) mbar_init(full + k, 1);
@@ -249,7 +251,8 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        ref[nt][c] = -1e30f;   // lower than any logit: the first one moves it
+        ref[nt][c] = kFirstReference;
+        if (gq == 0) bases[warp][8 * nt + 2 * tq + c] = 0.f;
         den[nt][c] = 0.f;
 #pragma unroll
         for (int k = 0; k < NG; ++k) zac[nt][k][c] = 0.f;
@@ -260,6 +263,8 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
         for (int i = 0; i < 4; ++i) acc[nt][j][i] = 0.f;
     }
 
+    bool far = false;        // a row of the warp has a base other than 0
+    __syncwarp();
     for (int st = s_lo; st < s_hi && !dead; ++st) {
       const uint32_t slot = ncons % kStages;
       {
@@ -337,7 +342,7 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
         }
       // ---- softmax weights
       float p[NT][2][2][2];
-      bool over = false;
+      bool over = far;         // rows with a base take the long way every time
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -353,20 +358,43 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
               over |= p[nt][bk][r][c] * top[bk][r] > kTop;
             }
       if (__any_sync(0xffffffffu, over)) {
+        far = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float m = -INFINITY;
+            float& base = bases[warp][8 * nt + 2 * tq + c];
+            const float from = base;
+            float mx = -INFINITY, m = -INFINITY;
+            over = false;
 #pragma unroll
             for (int bk = 0; bk < 2; ++bk)
 #pragma unroll
-              for (int r = 0; r < 2; ++r) m = fmaxf(m, x[nt][bk][r][c] + log2f(top[bk][r]));
+              for (int r = 0; r < 2; ++r) {
+                const float xv = x[nt][bk][r][c];
+                over |= ex2((xv - from) - ref[nt][c]) * top[bk][r] > kTop;
+                mx = fmaxf(mx, xv);
+                m = fmaxf(m, xv + log2f(top[bk][r]));
+              }
+            const bool move = __ballot_sync(0xffffffffu, over) & (0x11111111u << tq);     // some lane of the column
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            }
+            const float to = move ? row_base(from, mx, m) : from;
+            m = -INFINITY;
+#pragma unroll
+            for (int bk = 0; bk < 2; ++bk)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) m = fmaxf(m, (x[nt][bk][r][c] - to) + log2f(top[bk][r]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (m - ref[nt][c] > 15.f) {
-              const float to = ceilf(m) - 8.f, f = ex2(ref[nt][c] - to);
-              ref[nt][c] = to;
+            if (move) {
+              const RowRef now = {to, row_reference(m)};
+              const float f = ex2(move_exponent({from, ref[nt][c]}, now, 1.f));
+              ref[nt][c] = now.ref;
+              if (gq == 0) base = to;
               den[nt][c] *= f;
 #pragma unroll
               for (int k = 0; k < NG; ++k) zac[nt][k][c] *= f;
@@ -375,12 +403,14 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
                 acc[nt][j][c] *= f;
                 acc[nt][j][2 + c] *= f;
               }
-#pragma unroll
-              for (int bk = 0; bk < 2; ++bk)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) p[nt][bk][r][c] = ex2(x[nt][bk][r][c] - to);
             }
+            far |= __any_sync(0xffffffffu, to != 0.f);
+#pragma unroll
+            for (int bk = 0; bk < 2; ++bk)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) p[nt][bk][r][c] = ex2((x[nt][bk][r][c] - to) - ref[nt][c]);
           }
+        __syncwarp();      // the bases are written
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -430,6 +460,25 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
       }
     }
     __syncthreads();   // every warp is done with its ring: the merge may overlay it
+    if (far) {         // rows with a base: their sums to that reference, which fp32 holds
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float base = bases[warp][8 * nt + 2 * tq + c];
+          if (base == 0.f) continue;
+          const float f = ex2(ref[nt][c]);
+          ref[nt][c] = base;
+          den[nt][c] *= f;
+#pragma unroll
+          for (int k = 0; k < NG; ++k) zac[nt][k][c] *= f;
+#pragma unroll
+          for (int j = 0; j < 2 * NG; ++j) {
+            acc[nt][j][c] *= f;
+            acc[nt][j][2 + c] *= f;
+          }
+        }
+    }
 
     // ---- join the lanes of a column, then the warps
 #pragma unroll

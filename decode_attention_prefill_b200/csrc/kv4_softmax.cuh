@@ -41,5 +41,12 @@ PNMIX_BOTH float move_exponent(const RowRef& old, const RowRef& now, float fac) 
 // The reference in the log2 domain, for joining partial sums of a row.
 PNMIX_BOTH float reference_of(const RowRef& r, float fac) { return fmaf(r.base, fac, r.ref); }
 
+// The row kernel takes logits that are scaled already (fac 1) and weights their value scale as well:
+// 2^((x - base) - ref) times it stays within fp16.  Its reference after a move: base from the largest
+// logit mx and the largest m of logit + log2 of the token's value scale (within 2^-4 of the exact one
+// below 2^20), then ref from that m with base taken away, so no product is above 2^(8 + 2^-4).
+PNMIX_BOTH float row_base(float base, float mx, float m) { return base == 0.f && fabsf(m) < kFarLogit ? 0.f : mx; }
+PNMIX_BOTH float row_reference(float m) { return ceilf(m) - 8.f; }
+
 }  // namespace kv4
 }  // namespace pnmix

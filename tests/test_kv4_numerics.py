@@ -139,3 +139,42 @@ def test_attention_where_very_large_logits_grow(pm, T, amp):  # noqa: F811
     for j in range(T):
         want, tol = mean_of_tokens(v, [n - T + j])
         assert (np.abs(out[j] - want) <= tol).all(), (j, np.abs(out[j] - want).max())
+
+
+@pytest.mark.parametrize("T", [1, 4])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("vamp", [1e-5, 1.0, 2000.0])
+def test_attention_of_few_rows_where_logits_are_very_large(pm, T, D, vamp):  # noqa: F811
+    """As above for tiles of 8 and 16 rows, where the weights meet the fp16 range times a value scale:
+    one of the three tokens has values 64 times smaller than the others."""
+    r = np.random.default_rng(411)
+    n = 600
+    k, v = ref.bf16(r.standard_normal((n, 1, D)) * 0.05), rows(412, n, 1, D, vamp)
+    v[200] /= 64
+    base = ref.bf16(np.sign(r.standard_normal(D)) * (1 + r.random(D)))
+    hot = [3, 200, 300]
+    k[hot] = base
+    s = cached(pm, [n], [T], 4, 1, D, k, v)
+    want, tol = mean_of_tokens(v, hot)
+    for amp in [2.0 ** i for i in range(12, 40)] + [1e20, 1e29]:
+        q = ref.bf16(np.tile(base, (T, 4, 1)) * amp)
+        out = host(s.cache.attend(s.batch, dev(q)))
+        assert (np.abs(out - want) <= tol).all(), (amp, np.abs(out - want).max())
+    assert s.cache.read_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 4])
+def test_attention_of_few_rows_where_very_large_logits_grow(pm, T):  # noqa: F811
+    r = np.random.default_rng(413)
+    n, D = 150, 128
+    base = ref.bf16(r.standard_normal(D))
+    k = ref.bf16(1.05 ** np.arange(n)[:, None, None] * base * 0.05)
+    v = rows(414, n, 1, D) * (2.0 ** r.integers(-12, 6, (n, 1, 1))).astype(np.float32)
+    s = cached(pm, [n], [T], 4, 1, D, k, v)
+    for amp in [2.0 ** i for i in range(12, 40, 3)] + [1e20, 1e29]:
+        q = ref.bf16(np.tile(base, (T, 4, 1)) * amp)
+        out = host(s.cache.attend(s.batch, dev(q)))
+        for j in range(T):
+            want, tol = mean_of_tokens(v, [n - T + j])
+            assert (np.abs(out[j] - want) <= tol).all(), (amp, j, np.abs(out[j] - want).max())
+    assert s.cache.read_error() == 0
