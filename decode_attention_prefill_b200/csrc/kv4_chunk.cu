@@ -20,8 +20,9 @@
 //               channel to [1, 2): bf16 channels down to 2^-17 of it are exact, smaller ones are off
 //               by 2^-25 of it at most), B = key tile, both from shared memory; fp32 in TMEM
 //   softmax     one pass over S in TMEM, 32 columns at a time: p = 2^(x - m), summed in fp32
-//               and rounded to fp16 (2^-11 of each weight at most) over the S it came from.  The
-//               reference m moves only when a row's sum of 32 passes 2^15 (so no p is above the
+//               and rounded to fp16 (2^-11 of each weight, or 2^-30 of the largest) over the S it
+//               came from.  The
+//               reference m moves only when a row's sum of 32 passes 65504 (so no p is above the
 //               fp16 range, and no maximum has to be taken otherwise), once for these 32 at most:
 //               behind it their sum is in range by construction (kv4_softmax.cuh).  What the row
 //               has so far, in TMEM and out of it, is then rescaled
@@ -56,7 +57,7 @@ namespace {
 constexpr int kThreads = 608;
 constexpr int kTile = 128;                  // tokens of a key / value tile; rows of a stream
 constexpr uint32_t kCommitLimit = 1u << 22; // try_wait rounds of a wait inside the CTA
-constexpr float kTop = 32768.f;             // largest sum of 32 weights before the reference moves
+constexpr float kTop = 65504.f;             // largest sum of 32 weights before the reference moves: none is past fp16
 constexpr int kTmemO = 256;                 // TMEM columns: S (and P) of stream s at 128 s, O at 256 + 128 s
 
 // ---- tcgen05
@@ -502,14 +503,14 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
             uint32_t y[16];
             float mx = -INFINITY;
 #pragma unroll 1
-            for (int k = 32 * c; k < 32 * c + 32; k += 16) {
+            for (int k = 32 * c; k < kTile; k += 16) {      // the rest of the tile
               tmem_ld16(t_s + k, y);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 if (k + e < lim) mx = fmaxf(mx, __uint_as_float(y[e]));
             }
             float f = 1.f;
-            if (sum > kTop) {      // some weight is 2^10 at least
+            if (sum > kTop) {      // some weight is 2^10 and more
               const RowRef from = {*base, ref}, to = move_reference(from, mx, fac);
               f = ex2(move_exponent(from, to, fac));
               *base = to.base;

@@ -19,6 +19,15 @@ namespace kv4 {
 // the weights.  From 2^20 on the spacing of fp32 makes such a reference useless (at 2^28 it is 32,
 // and e may be 16 for the maximum itself), so the row's largest raw logit is taken away first: e is
 // then at most -ref by its sign alone, whatever the size of the logits.
+//
+// A move leaves the largest of the tile's weights at 2^5 to 2^6.  Weights become fp16, whose step is
+// 2^-24 at the least, so each is off by 2^-11 of itself or 2^-30 of the row's largest.  (With the
+// largest at 1, the first form, 2^-25 of it: a first token 2^21 times as strong as each of 30000 others
+// cost their sum 6 %.)  More room below leaves less above before the reference has to move again, and
+// each move reads O and writes it: 2 x 1024 tokens over 8192 cached ones, logits of a few outlier
+// channels, with 3, 4, 6 and 9 here 312, 314, 322 and 355 us (9 and a maximum over 32 columns instead
+// of the tile's rest: 415; all with moves from a sum of 2^15 on, at 65504 6 takes 319).
+constexpr float kRoom = 6.f;
 constexpr float kFarLogit = 1048576.f;
 constexpr float kFirstReference = -1e30f;   // lower than any logit: the first one moves it
 
@@ -26,11 +35,11 @@ struct RowRef {
   float base, ref;
 };
 
-// The reference after a move to the largest raw logit mx: no weight is above 2^(2^-5).
+// The reference after a move to the largest raw logit mx: no weight is above 2^(kRoom + 2^-5).
 PNMIX_BOTH RowRef move_reference(const RowRef& old, float mx, float fac) {
   const float t = mx * fac;
-  if (old.base == 0.f && fabsf(t) < kFarLogit) return {0.f, ceilf(t)};
-  return {mx, 0.f};
+  if (old.base == 0.f && fabsf(t) < kFarLogit) return {0.f, ceilf(t) - kRoom};
+  return {mx, -kRoom};
 }
 
 // log2 of what the row's sums so far are multiplied by in that move.

@@ -700,11 +700,19 @@ PNMIX_API pnmix_status pnmix_kv4_read(const pnmix_kv4_config* cfg, const pnmix_k
  *     out_r = sum_x softmax_x(q_r . k^_x * scale) v^_x  over x in [0, kv_len[b] - T + j]
  * for row j of the T rows of sequence b (so a row sees its own token, which was appended
  * before).  A row that sees no token (kv_len[b] < T - j) gets zeros.  q, out:
- * [n_tokens][Hq][head_dim], not overlapping (the same pointer: INVALID_ARG).  Sums and softmax in fp32, rounded to bf16 once;
- * the tensor cores' operands are fp16: query rows scaled by a power of two of their own, so that
- * channels down to 2^-17 of the row's largest are exact and smaller ones off by 2^-25 of it at
- * most (rows whose largest channel is 2^100 or more are outside the range); weights, and with
- * more than 16 rows per KV head keys and values too, rounded by up to 2^-11 of themselves.
+ * [n_tokens][Hq][head_dim], not overlapping (the same pointer: INVALID_ARG).  Sums and softmax in
+ * fp32, rounded to bf16 once; the tensor cores' operands are fp16:
+ *   queries   scaled by a power of two of each row, so that channels down to 2^-17 of the row's
+ *             largest are exact and smaller ones off by 2^-25 of it at most (rows whose largest
+ *             channel is 2^100 or more are outside the range);
+ *   weights   with more than 16 rows per tile off by 2^-11 of themselves or 2^-30 of the row's
+ *             largest.  With up to 16 the same (2^-33) of weight * s, which multiplies the code, while
+ *             weight * z is exact: where code * s and z cancel, what is left is off by 2^-11 of
+ *             weight * code * s;
+ *   keys and values   with more than 16 rows per tile code * s + z in fp16, off by 2^-11 of it.
+ * Logits are fp32: in the log2 domain one of size 2^n is off by about 2^(n - 22).  They may be as
+ * large as queries below 2^100 and the stored keys make them, while scale * log2(e) times a logit
+ * stays below 2^127.
  * A page outside the cache raises PNMIX_DEVERR_PAGE and the rows of its sequence are then
  * invalid.
  * The workspace (pnmix_kv4_workspace_bytes of the same cfg and batch, 256-byte aligned) needs

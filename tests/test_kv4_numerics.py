@@ -178,3 +178,41 @@ def test_attention_of_few_rows_where_very_large_logits_grow(pm, T):  # noqa: F81
             want, tol = mean_of_tokens(v, [n - T + j])
             assert (np.abs(out[j] - want) <= tol).all(), (amp, j, np.abs(out[j] - want).max())
     assert s.cache.read_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 4, 20, 140])
+@pytest.mark.parametrize("c,d", [(4.0, 0), (10.5, 0), (13.0, 0), (15.25, 0), (4.0, 0.5), (15.25, 0.5), (16.25, 0.5)])
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_one_strong_token_over_many_weak_ones(pm, T, c, d, sign):  # noqa: F811
+    """A first token whose weight is 2^5 to 2^21.3 times that of each of 30000 others, which hold an
+    odd channel each way: what the others add up to is kept.  160 units of one row tile or more, so a
+    CTA takes whole ones.  Keys and values are exact in 4 bits, so the logits are.  Off may be, in all
+    of 30000 weak terms alike: with up to 16 rows per tile the products of weights and scales by 2^-11 of
+    themselves or 2^-33 of the largest (2^-11.7 of the smallest here), with more the weights by 2^-30
+    of the largest (2^-8.7 of the smallest); values in fp16 not at all, the fp32 sums 2^-12, bf16 2^-8.
+    Where the strong token's zero is code * s + z = 15/16 - 15/16 (negative sign), the row kernel's
+    product weight * s is rounded to fp16 and its weight * z is not: 2^-11 of weight * 15/16."""
+    B, Hq, Hkv, D, n, page = 40, 16, 4, 64, 30000, 128
+    k, v = (np.zeros((n, Hkv, D), np.float32) for _ in range(2))
+    k[0, :, ::2] = 15 / 8
+    k[1:, :, 1::2] = 15 / 8
+    v[0, :, 1::2] = sign * 15 / 16
+    v[1:, :, ::2] = 15 / 16
+    cfg, pages = pm.KV4Config.make(Hq, Hkv, D, page, 1 / 64), -(-n // page)
+    cache = pm.KV4Cache(cfg, pages)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).repeat(B, 1)          # all of them share the pages
+    length = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    cache.append(pm.KV4Batch(length[:1], table[:1], n_tokens=n), dev(k), dev(v))
+    q = torch.zeros(B * T, Hq, D, dtype=torch.bfloat16, device=DEV)
+    q[:, :, ::2] = c
+    q[:, :, 1::2] = d
+    out = host(cache.attend(pm.KV4Batch(length, table, n_tokens=B * T), q)).reshape(B, T, Hq, D)
+    strong = np.exp(32 * 15 / 8 * c / 64)
+    weak = np.exp(32 * 15 / 8 * d / 64) * (n - T + np.arange(T))[:, None, None]
+    even = np.arange(D) % 2 == 0
+    want = np.where(even, 15 / 16 * weak, sign * 15 / 16 * strong) / (weak + strong)
+    tol = np.abs(want) * (2.0 ** -8 + (2.0 ** -10 if T < 20 else 2.0 ** -8.5))
+    if sign < 0 and T < 20:
+        tol = tol + even * 2.0 ** -11 * 15 / 16 * strong / (weak + strong)
+    assert (np.abs(out - want) <= tol).all(), np.abs(out / want - 1).max()
+    assert cache.read_error() == 0
