@@ -507,7 +507,7 @@ decode_kernel(const __grid_constant__ AttnArgs a) {
     __syncthreads();
     for (int i = tid; i < nrows * (D / 4); i += kThreads) {
       const int v = i / (D / 4), c4 = i - v * (D / 4);
-      float m = -1e30f, l = 0.f;
+      float m = kFirstReference, l = 0.f;
       float w[kWarps];
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
@@ -572,7 +572,7 @@ merge_kernel(const __grid_constant__ AttnArgs a, int RT) {
   const int v0 = blockIdx.y * kRows, r = threadIdx.x & (kRows - 1), c0 = threadIdx.x / kRows, v = v0 + r;
   if (v0 >= f.rows) return;
   constexpr int kC = C4 / kLanes;
-  float m = -1e30f, l = 0.f;
+  float m = kFirstReference, l = 0.f;
   float4 o[kC];
 #pragma unroll
   for (int i = 0; i < kC; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -582,7 +582,7 @@ merge_kernel(const __grid_constant__ AttnArgs a, int RT) {
       float4 t[AHEAD][kC];
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
-        x[k] = make_float2(-1e30f, 0.f);
+        x[k] = make_float2(kFirstReference, 0.f);
         if (k0 + k < n) {
           const float* p = part_of<D>(a.wk.part, slot_of(first + k0 + k, first), RT);
           x[k] = reinterpret_cast<const float2*>(p)[v];

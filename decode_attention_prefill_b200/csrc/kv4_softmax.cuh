@@ -29,7 +29,7 @@ namespace kv4 {
 // of the tile's rest: 415; all with moves from a sum of 2^15 on, at 65504 6 takes 319).
 constexpr float kRoom = 6.f;
 constexpr float kFarLogit = 1048576.f;
-constexpr float kFirstReference = -1e30f;   // lower than any logit: the first one moves it
+constexpr float kFirstReference = -3.4e38f;   // lower than any logit: the first one moves it
 
 struct RowRef {
   float base, ref;

@@ -325,3 +325,13 @@ def test_weights_of_moderate_logits_are_the_softmax(tmp_path):
     got = w / w.sum(1, keepdims=True)
     # exponents of up to 2^11 are off by 2^-14 of a bit at most, exp2f by a few 2^-24
     assert (np.abs(got - want) <= want * 2.0 ** -12 + 1e-30).all()
+
+
+@pytest.mark.parametrize("log2", [100, 110, 120])
+def test_a_row_whose_logits_are_all_very_low_keeps_its_weights(tmp_path, log2):
+    r = np.random.default_rng(500 + log2)
+    fac = (1 + r.random(1000)) * 2.0 ** r.integers(40, 60, 1000)
+    x = (-(1 + r.random((1000, 96))) * (2.0 ** log2 / fac)[:, None]).astype(np.float32)
+    worst, w = run_rows(tmp_path, x, fac)
+    assert np.isfinite(w).all() and (worst <= 32768).all()
+    assert (np.take_along_axis(w, x.argmax(1)[:, None], 1) >= 0.5).all()

@@ -216,3 +216,18 @@ def test_one_strong_token_over_many_weak_ones(pm, T, c, d, sign):  # noqa: F811
         tol = tol + even * 2.0 ** -11 * 15 / 16 * strong / (weak + strong)
     assert (np.abs(out - want) <= tol).all(), np.abs(out / want - 1).max()
     assert cache.read_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 4, 20, 140])
+@pytest.mark.parametrize("kamp", [1.0, 3000.0])
+def test_rows_whose_logits_are_all_very_low(pm, T, kamp):  # noqa: F811
+    """Equal logits of -1e31 and below are a softmax like any other."""
+    r = np.random.default_rng(421)
+    n, D = 700, 128
+    base = ref.bf16(np.sign(r.standard_normal(D)) * (1 + r.random(D)))
+    k, v = np.tile(ref.bf16(base * kamp), (n, 1, 1)), rows(422, n, 1, D)
+    s = cached(pm, [n], [T], 4, 1, D, k, v)
+    out = host(s.cache.attend(s.batch, dev(np.tile(ref.bf16(base * -5e29), (T, 4, 1)))))
+    for j in range(T):
+        want, tol = mean_of_tokens(v, np.arange(n - T + j + 1))
+        assert (np.abs(out[j] - want) <= tol).all(), (j, np.abs(out[j] - want).max())
