@@ -44,6 +44,8 @@
 // such chains only.  Tried and slower: sixteen softmax warps (324 us then, against 308), value
 // products by half tiles (373), 16- or 64-column loads and their double buffering, register
 // shares by role (setmaxnreg), a quarter or half of the exp2 as polynomials.
+#include <float.h>
+
 #include <atomic>
 
 #include "kv4_attn.cuh"
@@ -423,7 +425,8 @@ chunk_kernel(const __grid_constant__ ChunkArgs a) {
                 pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
           }
           // the row's owner takes its factor
-          const float mine = g.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+          // (not 0: a hidden column's -inf times it has to stay -inf)
+          const float mine = fmaxf(g.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), FLT_MIN);
           const float got = __shfl_sync(0xffffffffu, mine, lane & 7);
           if (part == ra) fac = got;
         }

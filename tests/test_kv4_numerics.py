@@ -231,3 +231,17 @@ def test_rows_whose_logits_are_all_very_low(pm, T, kamp):  # noqa: F811
     for j in range(T):
         want, tol = mean_of_tokens(v, np.arange(n - T + j + 1))
         assert (np.abs(out[j] - want) <= tol).all(), (j, np.abs(out[j] - want).max())
+
+
+@pytest.mark.parametrize("T", [1, 4, 20, 140])
+def test_a_scale_that_leaves_no_logit(pm, T):  # noqa: F811
+    """Queries and a softmax scale whose product is below fp32: every row is the mean of what it sees."""
+    n, D = 300, 128
+    k, v = rows(431, n, 1, D), rows(432, n, 1, D)
+    s = cached(pm, [n], [T], 4, 1, D, k, v)
+    cfg = pm.KV4Config.make(4, 1, D, 32, 1e-12)
+    cache = pm.KV4Cache(cfg, s.n_pages, buffer=s.cache.buffer)
+    out = host(cache.attend(s.batch, dev(rows(433, T, 4, D, 1e-36))))
+    for j in range(T):
+        want, tol = mean_of_tokens(v, np.arange(n - T + j + 1))
+        assert (np.abs(out[j] - want) <= tol).all(), (j, np.abs(out[j] - want).max())
