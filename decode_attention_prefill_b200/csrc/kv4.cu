@@ -264,9 +264,13 @@ pnmix_status pnmix_debug_kv4_stall(const pnmix_kv4_config* cfg, const pnmix_kv4_
 
 pnmix_status pnmix_kv4_read_error(const pnmix_kv4_cache* cache, int clear, uint32_t* host_error) {
   if (!cache || !cache->error || !host_error) return PNMIX_ERR_INVALID_ARG;
-  if (cudaMemcpy(host_error, cache->error, sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
+  // the calls before may be on streams that the default stream does not wait for, those behind as well
+  if (cudaDeviceSynchronize() != cudaSuccess ||
+      cudaMemcpy(host_error, cache->error, sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
     return PNMIX_ERR_CUDA;
-  if (clear && cudaMemset(cache->error, 0, sizeof(uint32_t)) != cudaSuccess) return PNMIX_ERR_CUDA;
+  if (clear && (cudaMemset(cache->error, 0, sizeof(uint32_t)) != cudaSuccess ||
+                cudaStreamSynchronize(nullptr) != cudaSuccess))
+    return PNMIX_ERR_CUDA;
   return *host_error ? PNMIX_ERR_DEVICE : PNMIX_OK;
 }
 

@@ -375,10 +375,9 @@ class KV4Cache:
         return self.buffer[:n].view(self.n_pages, c.n_kv_heads, c.page_tokens // 16, 20 * c.head_dim)
 
     def read_error(self, clear: bool = True) -> int:
-        """The device error word (waits for the device)."""
+        """The device error word, once all work on the device is done, on whatever stream."""
         val = ctypes.c_uint32(0)
         with torch.cuda.device(self.device):
-            torch.cuda.current_stream().synchronize()
             st = _lib.pnmix_kv4_read_error(self._refs[1], 1 if clear else 0, ctypes.byref(val))
         if st not in (OK, ERR_DEVICE):
             raise PNMixError(st, "pnmix_kv4_read_error")

@@ -1,0 +1,28 @@
+"""How the calls of the 4-bit paged cache behave around their arithmetic, on the GPU."""
+import numpy as np
+import pytest
+import torch
+
+from test_kv4 import DEV, Setup, dev, host, pm, rows  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("clear", [True, False])
+def test_the_error_word_waits_for_every_stream(pm, clear):  # noqa: F811
+    """A call that is still queued on a side stream is reported by the read that follows it, and not
+    once more by the next."""
+    s = Setup(pm, [100, 100], [1, 1], 4, 2, 128, 32)
+    s.fill()
+    q = dev(rows(11, s.n, 4, 128))
+    s.table[1, 2] = -5
+    bad = s.make_batch(s.kv_len, s.start)
+    assert s.cache.read_error() == 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)      # 50 ms and more
+    s.cache.attend(bad, q, stream=side)
+    assert s.cache.read_error(clear=clear) == pm.DEVERR_PAGE
+    assert s.cache.read_error() == (0 if clear else pm.DEVERR_PAGE)
+    assert s.cache.read_error() == 0
