@@ -372,8 +372,10 @@ class PNMixCache:
             .view(self.batch, self.cfg.n_kv_heads, 64)
 
     def read_error(self, clear: bool = True) -> int:
+        """The device error word, once all work on the device is done, on whatever stream."""
         val = ctypes.c_uint32(0)
-        st = _lib.pnmix_read_error(ctypes.byref(self.c), 1 if clear else 0, ctypes.byref(val))
+        with torch.cuda.device(self.buffer.device):
+            st = _lib.pnmix_read_error(ctypes.byref(self.c), 1 if clear else 0, ctypes.byref(val))
         if st not in (OK, ERR_DEVICE):
             raise PNMixError(st, "pnmix_read_error")
         return int(val.value)

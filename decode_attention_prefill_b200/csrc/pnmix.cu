@@ -464,12 +464,13 @@ pnmix_status pnmix_split_groups(const pnmix_config* cfg, int batch, const uint16
 
 pnmix_status pnmix_read_error(const pnmix_cache* cache, int clear, uint32_t* host_error) {
   if (!cache || !cache->error || !host_error) return PNMIX_ERR_INVALID_ARG;
-  cudaError_t e = cudaMemcpy(host_error, cache->error, sizeof(uint32_t), cudaMemcpyDeviceToHost);
-  if (e != cudaSuccess) return PNMIX_ERR_CUDA;
-  if (clear) {
-    e = cudaMemset(cache->error, 0, sizeof(uint32_t));
-    if (e != cudaSuccess) return PNMIX_ERR_CUDA;
-  }
+  // the calls before may be on streams that the default stream does not wait for, those behind as well
+  if (cudaDeviceSynchronize() != cudaSuccess ||
+      cudaMemcpy(host_error, cache->error, sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
+    return PNMIX_ERR_CUDA;
+  if (clear && (cudaMemset(cache->error, 0, sizeof(uint32_t)) != cudaSuccess ||
+                cudaStreamSynchronize(nullptr) != cudaSuccess))
+    return PNMIX_ERR_CUDA;
   return *host_error ? PNMIX_ERR_DEVICE : PNMIX_OK;
 }
 

@@ -525,7 +525,10 @@ PNMIX_API pnmix_status pnmix_debug_decode_stall(const pnmix_config* cfg, const u
                                                 void* workspace, size_t workspace_bytes, int skip_unit,
                                                 uint32_t wait_rounds, void* stream);
 
-/* Synchronously read (and, if clear != 0, zero) the device error word.  Host pointer out. */
+/*
+ * Read (and, if clear != 0, zero) the device error word, once all work on the device is done, on
+ * whatever stream; a clear is done on return.  Host pointer out.
+ */
 PNMIX_API pnmix_status pnmix_read_error(const pnmix_cache* cache, int clear, uint32_t* host_error);
 
 /* ================================================================================
@@ -736,10 +739,7 @@ PNMIX_API pnmix_status pnmix_debug_kv4_stall(const pnmix_kv4_config* cfg, const 
                                              const pnmix_rows* out, void* workspace, size_t workspace_bytes,
                                              int skip_seq, uint32_t wait_rounds, void* stream);
 
-/*
- * Read (and, if clear != 0, zero) the device error word, once all work on the device is done, on
- * whatever stream; a clear is done on return.  Host pointer out.
- */
+/* pnmix_read_error for this cache. */
 PNMIX_API pnmix_status pnmix_kv4_read_error(const pnmix_kv4_cache* cache, int clear, uint32_t* host_error);
 
 /* Static string for a status code. */

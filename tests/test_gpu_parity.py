@@ -815,3 +815,18 @@ def test_tcgen05_decode_is_repeatable():
     a = c.cache.attend_multi(q).clone()
     b = c.cache.attend_multi(q)
     assert torch.equal(a, b)
+
+
+def test_the_error_word_waits_for_every_stream():
+    """An append that is still queued on a side stream is reported by the read that follows it."""
+    c = Case(1, 4, 1, 64, capacity=64)
+    c.prefill()
+    assert c.cache.read_error() == 0
+    k, v = to_dev(c.kin[:, :, 0].copy()), to_dev(c.vin[:, :, 0].copy())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)      # 50 ms and more
+    c.cache.append(k, v, stream=side)
+    assert c.cache.read_error(clear=False) == 0x1
+    assert c.cache.read_error() == 0x1 and c.cache.read_error() == 0
