@@ -301,9 +301,9 @@ class KV4Cache:
 
     def append(self, batch: KV4Batch, k: torch.Tensor, v: torch.Tensor, stream=None):
         """Quantise rows k, v bf16 [n][Hkv][head_dim] (after RoPE) into the batch's places."""
+        ctx, s, named = self._on(batch, stream)
         kv = (batch.n_tokens, *self._kv)
         rk, rv = _pack(*_strides(k, kv, self.device, "k")), _pack(*_strides(v, kv, self.device, "v"))
-        ctx, s, named = self._on(batch, stream)
         with ctx:
             _check(_append(self._refs[0], batch.ref, rk, rv, self._refs[1], s), "pnmix_kv4_append")
         if named is not None:
@@ -315,13 +315,13 @@ class KV4Cache:
         """norm_rope of q and k and append of the rotated k and v in one pass; returns q_out."""
         if not isinstance(rope, Rope):
             raise TypeError("rope must be a Rope")
+        ctx, s, named = self._on(batch, stream)
         n, dev = batch.n_tokens, self.device
         qs, kv = (n, *self._q), (n, *self._kv)
         rq, rk, rv = _pack(*_strides(q, qs, dev, "q")), _pack(*_strides(k, kv, dev, "k")), _pack(*_strides(v, kv, dev, "v"))
         pos = _positions(positions, rope.n_axes, n, dev)
         D = qs[2]
         wq, wk = _weight(q_weight, D, dev, "q_weight"), _weight(k_weight, D, dev, "k_weight")
-        ctx, s, named = self._on(batch, stream)
         with ctx:
             q_out, oq = _out(q_out, qs, q, dev, "q_out")
             _check(_append_qkv(self._refs[0], _byref(rope), batch.ref, rq, rk, rv, wq, wk, pos, oq, self._refs[1], s),
@@ -333,8 +333,8 @@ class KV4Cache:
     def read(self, batch: KV4Batch, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
              stream=None):
         """The batch's rows as the cache holds them: (k, v) bf16 [n][Hkv][head_dim]."""
-        kv, dev = (batch.n_tokens, *self._kv), self.device
         ctx, s, named = self._on(batch, stream)
+        kv, dev = (batch.n_tokens, *self._kv), self.device
         with ctx:
             if k_out is None:
                 k_out = torch.empty(kv, dtype=torch.bfloat16, device=dev)
@@ -352,9 +352,9 @@ class KV4Cache:
         """Causal attention of q bf16 [n][Hq][head_dim] over the pages -> bf16, same shape.
         The workspace (kv4_workspace_bytes) is taken from torch's allocator for the call unless
         one is given."""
+        ctx, s, named = self._on(batch, stream)
         qs, dev = (batch.n_tokens, *self._q), self.device
         rq = _pack(*_strides(q, qs, dev, "q"))
-        ctx, s, named = self._on(batch, stream)
         with ctx:
             out, oo = _out(out, qs, q, dev, "out")
             if workspace is None:

@@ -335,3 +335,14 @@ def test_a_row_whose_logits_are_all_very_low_keeps_its_weights(tmp_path, log2):
     worst, w = run_rows(tmp_path, x, fac)
     assert np.isfinite(w).all() and (worst <= 32768).all()
     assert (np.take_along_axis(w, x.argmax(1)[:, None], 1) >= 0.5).all()
+
+
+@pytest.mark.parametrize("batch", [None, 3, object(), torch.zeros(1, dtype=torch.int32)])
+def test_calls_refuse_what_is_no_batch_by_type(batch):
+    c, x = object.__new__(pm.KV4Cache), torch.zeros(1, 1, 128, dtype=torch.bfloat16)
+    c.device, c._q, c._kv = torch.device("cuda", 0), (8, 128), (2, 128)
+    rope = pm.Rope.make(128)
+    for call in (lambda: c.append(batch, x, x), lambda: c.append_qkv(batch, rope, x, x, x, x), lambda: c.read(batch),
+                 lambda: c.attend(batch, x)):
+        with pytest.raises(TypeError, match="KV4Batch"):
+            call()
