@@ -262,13 +262,14 @@ class KV4Batch:
 
 class KV4Cache:
     """The pages of one layer.  `buffer`: uint8 memory to use, 256-byte aligned and at least
-    kv4_cache_bytes long (its contents stay); without it zeroed memory is taken."""
+    kv4_cache_bytes long (its contents stay); without it zeroed memory is taken.  What a cache was
+    made with stays: `cfg` gives a copy."""
 
     def __init__(self, cfg: KV4Config, n_pages: int, device="cuda", buffer: torch.Tensor | None = None):
         if not isinstance(cfg, KV4Config):
             raise TypeError("cfg must be a KV4Config")
         cfg = KV4Config.from_buffer_copy(cfg)      # what the caller does with theirs later changes no call
-        self.cfg, self.n_pages = cfg, n_pages
+        self._cfg, self.n_pages = cfg, n_pages
         nbytes = kv4_cache_bytes(cfg, n_pages)
         if buffer is None:
             buffer = torch.zeros(nbytes, dtype=torch.uint8, device=device)
@@ -278,8 +279,17 @@ class KV4Cache:
         self.c = _Cache()
         _check(_lib.pnmix_kv4_cache_init(ctypes.byref(cfg), n_pages, buffer.data_ptr(), buffer.numel(),
                                          ctypes.byref(self.c)), "pnmix_kv4_cache_init")
-        self._refs = (ctypes.byref(cfg), ctypes.byref(self.c))
         self._q, self._kv = (cfg.n_q_heads, cfg.head_dim), (cfg.n_kv_heads, cfg.head_dim)
+        self._refs = (ctypes.byref(cfg), ctypes.byref(self.c))
+
+    @property
+    def cfg(self) -> KV4Config:
+        return KV4Config.from_buffer_copy(self._cfg)
+
+    def __setattr__(self, name, value):
+        if "_refs" in self.__dict__:       # the calls' pointers and the tensors' shapes belong together
+            raise AttributeError(f"{name} of a KV4Cache stays as it was made; make another cache")
+        super().__setattr__(name, value)
 
     def reset(self, stream=None):
         """Zero the pages and the error word."""
@@ -370,7 +380,7 @@ class KV4Cache:
 
     def pages(self) -> torch.Tensor:
         """uint8 view [n_pages][Hkv][blocks][20 * head_dim] (for tests and inspection)."""
-        c = self.cfg
+        c = self._cfg
         n = self.n_pages * c.n_kv_heads * (c.page_tokens // 16) * 20 * c.head_dim
         return self.buffer[:n].view(self.n_pages, c.n_kv_heads, c.page_tokens // 16, 20 * c.head_dim)
 

@@ -26,3 +26,19 @@ def test_the_error_word_waits_for_every_stream(pm, clear):  # noqa: F811
     assert s.cache.read_error(clear=clear) == pm.DEVERR_PAGE
     assert s.cache.read_error() == (0 if clear else pm.DEVERR_PAGE)
     assert s.cache.read_error() == 0
+
+
+def test_a_cache_cannot_be_changed_from_outside(pm):  # noqa: F811
+    """Its heads, pages and memory are what its calls check the tensors against."""
+    s = Setup(pm, [40], [2], 8, 2, 128, 16)
+    s.fill()
+    q = dev(rows(21, 2, 8, 128))
+    want, pages = s.cache.attend(s.batch, q), s.cache.pages().clone()
+    for name, value in (("n_q_heads", 64), ("n_kv_heads", 8), ("head_dim", 64), ("page_tokens", 128)):
+        setattr(s.cache.cfg, name, value)              # of a copy
+        assert getattr(s.cache.cfg, name) != value
+    for name, value in (("cfg", pm.KV4Config.make(16, 2)), ("buffer", s.cache.buffer[:256]), ("n_pages", 100),
+                        ("device", torch.device("cpu"))):
+        with pytest.raises(AttributeError):
+            setattr(s.cache, name, value)
+    assert torch.equal(s.cache.attend(s.batch, q), want) and torch.equal(s.cache.pages(), pages)
