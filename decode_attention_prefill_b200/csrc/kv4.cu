@@ -135,6 +135,9 @@ pnmix_status pnmix_norm_rope(const pnmix_rope* rope, int n_tokens, int n_q_heads
     PNMIX_TRY(check_rows(k, n_tokens, n_k_heads, rope->head_dim, false));
     PNMIX_TRY(check_rows(k_out, n_tokens, n_k_heads, rope->head_dim, true));
   }
+  // an output may be its own input; over another tensor it would be read after it was written
+  if (n_q_heads && n_k_heads && (q_out->data == k_out->data || q_out->data == k->data || k_out->data == q->data))
+    return PNMIX_ERR_INVALID_ARG;
   return cuda_status(launch_norm_rope(*rope, n_tokens, n_q_heads, n_k_heads, n_q_heads ? *q : none,
                                       n_k_heads ? *k : none, n_q_heads ? q_weight : nullptr,
                                       n_k_heads ? k_weight : nullptr, positions, n_q_heads ? *q_out : none,
@@ -204,6 +207,7 @@ pnmix_status pnmix_kv4_append_qkv(const pnmix_kv4_config* cfg, const pnmix_rope*
   PNMIX_TRY(check_rows(k, bt.n_tokens, g.Hkv, g.D, false));
   PNMIX_TRY(check_rows(v, bt.n_tokens, g.Hkv, g.D, false));
   PNMIX_TRY(check_rows(q_out, bt.n_tokens, g.Hq, g.D, true));
+  if (q_out->data == k->data || q_out->data == v->data) return PNMIX_ERR_INVALID_ARG;
   return cuda_status(launch_append_qkv(g, bt, *rope, *q, *k, *v, q_weight, k_weight, positions, *q_out,
                                        static_cast<cudaStream_t>(stream)));
 }
@@ -218,6 +222,7 @@ pnmix_status pnmix_kv4_read(const pnmix_kv4_config* cfg, const pnmix_kv4_batch* 
   if (bt.n_tokens == 0) return PNMIX_OK;
   PNMIX_TRY(check_rows(k_out, bt.n_tokens, g.Hkv, g.D, true));
   PNMIX_TRY(check_rows(v_out, bt.n_tokens, g.Hkv, g.D, true));
+  if (k_out->data == v_out->data) return PNMIX_ERR_INVALID_ARG;
   return cuda_status(launch_read(g, bt, *k_out, *v_out, static_cast<cudaStream_t>(stream)));
 }
 

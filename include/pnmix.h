@@ -644,7 +644,8 @@ typedef struct {
  * and then to bf16.  n_tokens rows (0 allowed: nothing is done); q and
  * q_out have n_q_heads heads, k and k_out n_k_heads; either head count may be 0, and its
  * pointers are then not looked at.  positions: int32 [n_axes][n_tokens], any values.
- * An output may be its own input (same pointer and strides), otherwise it overlaps none.
+ * An output may be its own input (same pointer and strides), otherwise it overlaps no other tensor
+ * (the same pointer: INVALID_ARG).
  * Errors: INVALID_ARG (null pointers, negative sizes, an axis >= n_axes, output strides
  * that let rows overlap), UNSUPPORTED (head_dim, rot_dim or n_axes outside the above),
  * ALIGNMENT (pointers not 16-byte aligned or strides not multiples of 8).
@@ -681,7 +682,8 @@ PNMIX_API pnmix_status pnmix_kv4_append(const pnmix_kv4_config* cfg, const pnmix
  * pnmix_norm_rope of q and k and pnmix_kv4_append of the rotated keys and v in one pass: the
  * cache and q_out get the same bits as from the two calls (the keys are rounded to bf16
  * between them).  q, k, v: usually three views of one projection.  positions: int32
- * [n_axes][n_tokens], apart from the places in the cache.  rope->head_dim is the cache's.
+ * [n_axes][n_tokens], apart from the places in the cache.  rope->head_dim is the cache's.  q_out may
+ * be q, and overlaps neither k nor v (the same pointer: INVALID_ARG).
  */
 PNMIX_API pnmix_status pnmix_kv4_append_qkv(const pnmix_kv4_config* cfg, const pnmix_rope* rope,
                                             const pnmix_kv4_batch* batch, const pnmix_rows* q,
@@ -691,7 +693,8 @@ PNMIX_API pnmix_status pnmix_kv4_append_qkv(const pnmix_kv4_config* cfg, const p
                                             pnmix_kv4_cache* cache, void* stream);
 
 /*
- * Read the batch's rows back: bf16(code * s + z) into k_out and v_out.  A row without a
+ * Read the batch's rows back: bf16(code * s + z) into k_out and v_out, which do not overlap (the
+ * same pointer: INVALID_ARG).  A row without a
  * place gets zeros (and raises the bits of pnmix_kv4_append).
  */
 PNMIX_API pnmix_status pnmix_kv4_read(const pnmix_kv4_config* cfg, const pnmix_kv4_batch* batch,

@@ -346,3 +346,19 @@ def test_calls_refuse_what_is_no_batch_by_type(batch):
                  lambda: c.attend(batch, x)):
         with pytest.raises(TypeError, match="KV4Batch"):
             call()
+
+
+@no_gpu
+def test_outputs_over_other_tensors_are_refused():
+    """The same memory for two outputs, or for an output and another tensor's input."""
+    cfg = pm.KV4Config.make(8, 8)
+    c, b, L, rope = cache(cfg), batch(), pm._lib, pm.Rope.make(128)
+    w, x, y, z = (rows(data=P + (i << 30)) for i in range(4))
+    assert L.pnmix_kv4_read(B(cfg), B(b), B(c), B(x), B(x), None) == pm.ERR_INVALID_ARG
+
+    def nr(q, k, qo, ko):
+        return L.pnmix_norm_rope(B(rope), 6, 8, 8, B(q), B(k), None, None, P, B(qo), B(ko), None)
+    assert nr(w, x, y, y) == nr(w, x, x, y) == nr(w, x, y, w) == nr(w, x, x, w) == pm.ERR_INVALID_ARG
+    for out in (x, y):
+        assert L.pnmix_kv4_append_qkv(B(cfg), B(rope), B(b), B(w), B(x), B(y), None, None, P, B(out), B(c), None) \
+            == pm.ERR_INVALID_ARG
