@@ -25,6 +25,13 @@ from . import OK, ERR_DEVICE, PNMixError, _check, _lib
 _vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 
 
+def _count(x, name: str) -> int:
+    """A size that the C structures hold: ctypes would keep its low 32 bits without a word."""
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 class KV4Config(ctypes.Structure):
     """pnmix_kv4_config: heads and pages of a 4-bit cache."""
     _fields_ = [("head_dim", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
@@ -33,7 +40,8 @@ class KV4Config(ctypes.Structure):
     @classmethod
     def make(cls, n_q_heads: int, n_kv_heads: int, head_dim: int = 128, page_tokens: int = 64,
              softmax_scale: float = 0.0) -> "KV4Config":
-        return cls(head_dim, n_q_heads, n_kv_heads, page_tokens, softmax_scale)
+        return cls(_count(head_dim, "head_dim"), _count(n_q_heads, "n_q_heads"), _count(n_kv_heads, "n_kv_heads"),
+                   _count(page_tokens, "page_tokens"), softmax_scale)
 
 
 class Rope(ctypes.Structure):
@@ -58,7 +66,7 @@ class Rope(ctypes.Structure):
             raise ValueError("inv_freq and axes hold rot_dim / 2 entries, at most 128")
         if any(not 0 <= x <= 3 for x in axes):
             raise ValueError("axes are 0 .. 3")
-        r = cls(head_dim, rot_dim, int(interleaved), max(axes, default=0) + 1, eps)
+        r = cls(_count(head_dim, "head_dim"), _count(rot_dim, "rot_dim"), int(interleaved), max(axes, default=0) + 1, eps)
         r.inv_freq[:len(inv_freq)] = inv_freq
         r.axis[:len(axes)] = axes
         return r
@@ -249,7 +257,7 @@ class KV4Batch:
         B, dev = kv_len.numel(), kv_len.device
         if max_q is None:
             max_q = n_tokens if q_start is not None else n_tokens // B
-        c = _Batch(B, n_tokens, page_table.shape[1], max_q,
+        c = _Batch(B, _count(n_tokens, "n_tokens"), page_table.shape[1], _count(max_q, "max_q"),
                    None if q_start is None else _ints(q_start, (B + 1,), dev, "q_start"),
                    _ints(kv_len, (B,), dev, "kv_len"),
                    _ints(page_table, (B, page_table.shape[1]), dev, "page_table"))
@@ -396,7 +404,8 @@ class KV4Cache:
 
 def kv4_cache_bytes(cfg: KV4Config, n_pages: int) -> int:
     out = _sz(0)
-    _check(_lib.pnmix_kv4_cache_bytes(ctypes.byref(cfg), n_pages, ctypes.byref(out)), "pnmix_kv4_cache_bytes")
+    _check(_lib.pnmix_kv4_cache_bytes(ctypes.byref(cfg), _count(n_pages, "n_pages"), ctypes.byref(out)),
+           "pnmix_kv4_cache_bytes")
     return int(out.value)
 
 

@@ -362,3 +362,20 @@ def test_outputs_over_other_tensors_are_refused():
     for out in (x, y):
         assert L.pnmix_kv4_append_qkv(B(cfg), B(rope), B(b), B(w), B(x), B(y), None, None, P, B(out), B(c), None) \
             == pm.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("big", [(1 << 32) + 8, 1 << 31, -(1 << 32) + 8])
+def test_sizes_past_32_bits_are_refused(big):
+    """A C field would keep their low bits: 2^32 + 8 heads were 8."""
+    good = dict(n_q_heads=8, n_kv_heads=8, head_dim=128, page_tokens=64)
+    for name in good:
+        with pytest.raises(ValueError, match=name):
+            pm.KV4Config.make(**{**good, name: big})
+    with pytest.raises(ValueError, match="n_pages"):
+        pm.kv4_cache_bytes(pm.KV4Config.make(**good), big)
+    with pytest.raises(ValueError, match="head_dim"):
+        pm.Rope.make(big, 64)
+    i32 = dict(dtype=torch.int32)
+    for kw in (dict(n_tokens=big), dict(n_tokens=8, max_q=big)):
+        with pytest.raises(ValueError, match=list(kw)[-1]):
+            pm.KV4Batch(torch.ones(2, **i32), torch.zeros(2, 3, **i32), **kw)
