@@ -245,3 +245,14 @@ def test_a_scale_that_leaves_no_logit(pm, T):  # noqa: F811
     for j in range(T):
         want, tol = mean_of_tokens(v, np.arange(n - T + j + 1))
         assert (np.abs(out[j] - want) <= tol).all(), (j, np.abs(out[j] - want).max())
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,T,lens", [(128, 4, 1, 30, [20000]), (64, 4, 2, 70, [9000, 300]),
+                                             (128, 8, 2, 140, [6000, 200]), (128, 28, 4, 5, [8000, 5000, 6])])
+def test_many_rows_over_long_contexts(pm, D, Hq, Hkv, T, lens):  # noqa: F811
+    """Tiles of 128 and 256 rows (the last: 16) whose units many CTAs share, against the definition."""
+    s = Setup(pm, lens, [min(T, n) for n in lens], Hq, Hkv, D, 64)
+    s.fill(441)
+    q = rows(442, s.n, Hq, D)
+    s.check_attention(q, s.cache.attend(s.batch, dev(q)))
+    assert s.cache.read_error() == 0
