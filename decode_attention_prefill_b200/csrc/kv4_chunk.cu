@@ -37,11 +37,12 @@
 // stores of neighbouring lanes lie side by side.
 //
 // Measured: 2 x 1024 tokens of 32 query and 8 KV heads (head_dim 128) over 8192 cached ones, the
-// merge included, 315 us or 820 TFLOP/s, half of what a library product of 8192^3 reaches here
-// (floor 156 us).  At 1 x 1024 the kernel takes 172 us with 39 % of the tensor and of the exp2
-// pipe busy, the warps waiting for TMEM loads: a stream's tile is a chain of products, their
-// commit, four rounds of load, exp2 and store, and the next products, and TMEM has room for two
-// such chains only.  Tried and slower: sixteen softmax warps (324 us then, against 308), value
+// merge included, 319 to 327 us by graph replay or 800 TFLOP/s, half of what a library product of
+// 8192^3 reaches here (floor 156 us).  At 1 x 1024 the kernel takes 187 us under the profiler with 38 %
+// of the tensor and of the exp2 pipe busy, the warps waiting for TMEM loads: a stream's tile is a
+// chain of products, their commit, four rounds of load, exp2 and store, and the next products.  TMEM
+// is full with two such chains as they stand (the half of a stream's logits that its weights do not
+// lie over stays idle meanwhile).  Tried and slower: sixteen softmax warps (324 us then, against 308), value
 // products by half tiles (373), 16- or 64-column loads and their double buffering, register
 // shares by role (setmaxnreg), a quarter or half of the exp2 as polynomials.
 #include <float.h>

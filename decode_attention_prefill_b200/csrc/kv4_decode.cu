@@ -30,10 +30,10 @@
 // channel is in [2^13, 2^14): every bf16 channel down to 2^-24 of it is exact in fp16.
 //
 // Measured, the merge included: one token of 16 sequences of 32768 with 32 query and 8 KV heads
-// (head_dim 128, so half of a column tile is empty) 142 us, 4.7 TB/s or 72 % of a plain copy.  At
-// half the length 52 % of DRAM and 51 % of the integer pipe are busy at 2.4 instructions a cycle:
-// the unpacking, two cycles an instruction, runs beside the copies but does not hide behind them
-// entirely.  Tried and not faster: the blocks of a stage unrolled at four CTAs per SM (152 us),
+// (head_dim 128, so half of a column tile is empty) 142 us by graph replay, 4.7 TB/s or 72 % of a
+// plain copy.  At half the length 51 % of DRAM and 52 % of the integer pipe are busy at 2.4
+// instructions a cycle: nothing is full, and twelve warps per SM do not hide each other's latency
+// (the `wait` of dependent instructions is the largest stall).  Tried and not faster: the blocks of a stage unrolled at four CTAs per SM (152 us),
 // warps without work leaving early.
 #include <atomic>
 
@@ -677,7 +677,9 @@ constexpr int kMaxCtas = 1024;
 // rows per token and KV head, 8 heads:  64 tokens of 64 sequences, 4K cached, 127 against 363 us;
 // a chunk of 256 tokens at 8K among 127 single ones at 2K (12 rows on the average) 353 against
 // 437 us; but a chunk of 128 at 32K among 31 single ones at 512 (20 rows) 436 against 170 us, and
-// of 64 among 63 (8 rows) 244 against 153 us.  So up to 16, one tile of most sequences.
+// of 64 among 63 (8 rows) 244 against 153 us.  So up to 16, one tile of most sequences.  (All of it
+// measured before the many-row kernel's reference stood lower, which costs it 2 to 4 %, at head_dim 64
+// 10 %, and before the row kernel's logits had a base, 1 %.)
 static int tile_rows(const Geo& g, const Batch& bt) {
   const int most = g.G * bt.max_q;
   const double mean = static_cast<double>(g.G) * bt.n_tokens / bt.B;

@@ -38,6 +38,7 @@ constexpr int kInThreads = 128, kOutThreads = 256;
 constexpr int kInRows = kInThreads / 4, kOutRows = kOutThreads / 4;   // rows a CTA works on at once
 constexpr int kMaxTok = 16;                 // tokens per CTA at most
 constexpr uint32_t kOnes = 0x3F803F80u;     // 1, 1 in bf16
+constexpr int kSms = 148;                   // of a B200: small calls are cut so that each has work
 
 // Sequence of packed row `row`: the last b with q_start[b] <= row, or -1 for a row outside
 // every sequence.  Called by a whole warp.
@@ -267,12 +268,13 @@ __device__ __forceinline__ void turn_of(int pos, float freq, double& c, double& 
 
 // ROPE: q and k rows are normed and rotated.  QUANT: k and v rows go to the cache (otherwise
 // k rows are stored like q's).
-// CTAs per SM.  Rotating kernels of 128 channels: six (80 registers; up to 32 registers' worth of
-// stores spill once a row).  At seven the fp64 of the keys spills inside: 94 instead of 66 us for the norm of 16384 tokens of 32 + 8 heads, 28.6 instead of 24.0 us
-// for the fused write of 3900 ragged tokens of 28 + 4 + 4 heads; five take 68 and 26.  (All rows in
-// fp32 at seven took 58 and 21 us.)  64 channels: seven, which is what 72 registers leave room for.
-// The plain write: eight (64 registers); ten take 28.7 instead of 26.7 us.  256 channels: three, the
-// registers that they need.
+// CTAs per SM.  Rotating kernels of 128 channels: six (80 registers, 16 to 128 bytes of spills in four
+// of the six forms).  At seven the fp64 of the keys spills 250 bytes: 94 instead of 66 us for the norm
+// of 16384 tokens of 32 + 8 heads, 28.6 instead of 24.0 us for the fused write of 3900 ragged tokens of
+// 28 + 4 + 4 heads; five take 68 and 26.  (All rows in fp32 at seven took 58 and 21 us.)  64 channels:
+// seven, which is what 72 registers leave room for.  The plain write: eight (64 registers); ten took
+// 28.7 instead of 26.7 us, before two lanes an instruction.  256 channels: three, the registers that
+// they need.
 template <int D, bool ROPE, bool QUANT, int PAIRS>
 __global__ void __launch_bounds__(kInThreads, D == 256 ? 3 : !ROPE ? 8 : D == 128 ? 6 : 7)
 rows_in_kernel(const __grid_constant__ IoArgs a) {
@@ -661,7 +663,7 @@ rows_out_kernel(const __grid_constant__ OutArgs a) {
 // 55, 54 and 55 us.
 int token_shift(int n_tokens, int most) {
   int s = most;
-  while (s > 0 && (n_tokens >> s) < 4 * 148) --s;
+  while (s > 0 && (n_tokens >> s) < 4 * kSms) --s;
   return s;
 }
 
@@ -762,10 +764,10 @@ cudaError_t launch_read(const Geo& g, const Batch& bt, const pnmix_rows& k, cons
   a.v_hs = v.head_stride;
   // tokens inner: the rows of a block lie together; few tokens leave room for more CTAs in y
   a.tok_shift = 4;
-  while (a.tok_shift > 0 && (bt.n_tokens >> a.tok_shift) < 148) --a.tok_shift;
+  while (a.tok_shift > 0 && (bt.n_tokens >> a.tok_shift) < kSms) --a.tok_shift;
   const int x = (bt.n_tokens + (1 << a.tok_shift) - 1) >> a.tok_shift, rows = 2 * g.Hkv;
   a.rows_y = max(1, 2 * kOutRows >> a.tok_shift);
-  while (a.rows_y < rows && static_cast<long long>(x) * ((rows + a.rows_y - 1) / a.rows_y) > 148 * 16) a.rows_y *= 2;
+  while (a.rows_y < rows && static_cast<long long>(x) * ((rows + a.rows_y - 1) / a.rows_y) > kSms * 16) a.rows_y *= 2;
   const dim3 grid(x, (rows + a.rows_y - 1) / a.rows_y);
   if (g.D == 64)
     rows_out_kernel<64><<<grid, kOutThreads, 0, s>>>(a);

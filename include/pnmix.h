@@ -592,7 +592,7 @@ typedef struct {
 /*
  * The sequences of one call.  Token tensors are packed: sequence b owns the rows
  * [q_start[b], q_start[b+1]) of every one, in order of position; rows from q_start[batch]
- * on (padding) are neither read nor written.  Its newest row is position kv_len[b] - 1, so
+ * on (padding) are not written, and what they hold changes nothing.  Its newest row is position kv_len[b] - 1, so
  * with T rows row j is position kv_len[b] - T + j.  Position x of sequence b is token
  * x % page_tokens of page page_table[b][x / page_tokens].
  * The arrays are device memory, read when the call runs.  What they hold cannot be checked
@@ -721,6 +721,10 @@ PNMIX_API pnmix_status pnmix_kv4_read(const pnmix_kv4_config* cfg, const pnmix_k
  * stays below 2^127.
  * A page outside the cache raises PNMIX_DEVERR_PAGE and the rows of its sequence are then
  * invalid.
+ * One tile form serves the whole call: 8, 16, 128 or 256 rows per KV head, chosen from max_q and from
+ * n_tokens / batch (padding rows count in it), which is all that the host knows.  Calls that mix one
+ * long chunk with many single tokens can take 1.6 times as long as with the other form; a call for
+ * each kind avoids that.
  * The workspace (pnmix_kv4_workspace_bytes of the same cfg and batch, 256-byte aligned) needs
  * no initial content and keeps none; calls that may run at the same time need one each.
  */
