@@ -295,7 +295,8 @@ class KV4Cache:
         return KV4Config.from_buffer_copy(self._cfg)
 
     def __setattr__(self, name, value):
-        if "_refs" in self.__dict__:       # the calls' pointers and the tensors' shapes belong together
+        # the calls' pointers and the tensors' shapes belong together
+        if "_refs" in self.__dict__ and (name in self.__dict__ or name == "cfg"):
             raise AttributeError(f"{name} of a KV4Cache stays as it was made; make another cache")
         super().__setattr__(name, value)
 

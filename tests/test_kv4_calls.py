@@ -41,4 +41,5 @@ def test_a_cache_cannot_be_changed_from_outside(pm):  # noqa: F811
                         ("device", torch.device("cpu"))):
         with pytest.raises(AttributeError):
             setattr(s.cache, name, value)
+    s.cache.layer = 3                                  # a name of the caller's own
     assert torch.equal(s.cache.attend(s.batch, q), want) and torch.equal(s.cache.pages(), pages)
