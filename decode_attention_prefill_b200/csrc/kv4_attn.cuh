@@ -188,8 +188,10 @@ __device__ __forceinline__ const Plan& build_plan(const Geo& g, const Batch& bt,
 
 // Calls fn(piece) for every piece of this CTA, in order, until it returns false.  The piece and
 // where to go on lie in shared memory (`at`, of the calling warp), so that they hold no
-// registers while fn works.  SOLO: one lane calls it, else a whole warp.  `writer`: the one
-// thread that notes the shared unit for the merge.
+// registers while fn works.  A sequence's rows and length are read again for each piece.  They are
+// not to change while a call runs; where they do all the same, a piece that is no longer there ends
+// the walk, and none lies outside the tensors, the pages or the workspace.  SOLO: one lane calls it,
+// else a whole warp.  `writer`: the one thread that notes the shared unit for the merge.
 struct PieceSlot {
   Piece p;
   long long next;
@@ -217,12 +219,14 @@ __device__ __forceinline__ void for_each_piece(const Geo& g, const Batch& bt, in
     bool bad = false;
     Piece p;
     p.b = lo;
-    seq_rows(bt, lo, p.start, p.T);
+    if (!seq_rows(bt, lo, p.start, p.T)) return;
     p.len = seq_len(bt, g.page_shift, lo, bad);
     SeqCost c = seq_cost(g.G, RT, p.T, p.len);
     c.base += lead;
     const long long head = c.before(c.n), seq = plan.before(lo, bt.B);
-    p.h = static_cast<int>((x - seq) / head);
+    const long long h = (x - seq) / max(head, 1ll);
+    if (c.n < 1 || h >= g.Hkv) return;
+    p.h = static_cast<int>(h);
     const long long hstart = seq + p.h * head;
     int t0 = 0, t1 = c.n - 1;     // the last tile that starts at or before x
     while (t0 < t1) {
@@ -233,7 +237,7 @@ __device__ __forceinline__ void for_each_piece(const Geo& g, const Batch& bt, in
     p.tile = t0;
     const long long ustart = hstart + c.before(t0), uend = hstart + c.before(t0 + 1);
     const long long xe = uend < e ? uend : e;
-    const int first = cta_of_token(ustart, X, N), last = cta_of_token(uend - 1, X, N);
+    const int first = cta_of_token(ustart, X, N), last = cta_of_token(min(uend, X) - 1, X, N);
     p.lo = static_cast<int>(max(x - ustart - lead, 0ll));
     p.hi = static_cast<int>(max(xe - ustart - lead, 0ll));
     p.whole = first == last;

@@ -595,8 +595,9 @@ typedef struct {
  * on (padding) are not written, and what they hold changes nothing.  Its newest row is position kv_len[b] - 1, so
  * with T rows row j is position kv_len[b] - T + j.  Position x of sequence b is token
  * x % page_tokens of page page_table[b][x / page_tokens].
- * The arrays are device memory, read when the call runs.  What they hold cannot be checked
- * on the host.  The error word says what was wrong (see the bits above), and memory outside
+ * The arrays are device memory, read when the call runs, and stay as they are until it is done
+ * (changed meanwhile they make its results invalid).  What they hold cannot be checked on the
+ * host.  The error word says what was wrong (see the bits above), and memory outside
  * the tensors and the pages is never touched: lengths are clamped to [0, max_pages *
  * page_tokens]; with a q_start that is not ascending within [0, n_tokens], or a sequence of
  * more than max_q rows, pnmix_kv4_attention does nothing, and the other calls take rows for

@@ -43,3 +43,29 @@ def test_a_cache_cannot_be_changed_from_outside(pm):  # noqa: F811
             setattr(s.cache, name, value)
     s.cache.layer = 3                                  # a name of the caller's own
     assert torch.equal(s.cache.attend(s.batch, q), want) and torch.equal(s.cache.pages(), pages)
+
+
+@pytest.mark.parametrize("T", [1, 4, 20, 70])
+def test_lengths_that_change_under_a_call(pm, T):  # noqa: F811
+    """The caller's mistake, a host that copies the next step's lengths while a call runs: what that
+    call gives is not defined, but it ends, and the next one is right."""
+    B = 24
+    lens = [2000 + 40 * i for i in range(B)]
+    s = Setup(pm, lens, [T] * B, 4, 2, 64, 32)
+    s.fill()
+    q = dev(rows(31, s.n, 4, 64))
+    want = s.cache.attend(s.batch, q)
+    first = s.batch.kv_len.clone()
+    hosts = [torch.tensor(x, dtype=torch.int32).pin_memory() for x in ([0] * B, lens, [1] * B, lens[::-1])]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(12):
+            with torch.cuda.stream(side):
+                s.batch.kv_len.copy_(hosts[i % 4], non_blocking=True)
+            if i % 3 == 0:
+                s.cache.attend(s.batch, q)
+    torch.cuda.synchronize()
+    s.batch.kv_len.copy_(first)
+    assert not s.cache.read_error() & ~pm.DEVERR_BATCH
+    assert torch.equal(s.cache.attend(s.batch, q), want) and s.cache.read_error() == 0
