@@ -37,7 +37,7 @@
 // stores of neighbouring lanes lie side by side.
 //
 // Measured: 2 x 1024 tokens of 32 query and 8 KV heads (head_dim 128) over 8192 cached ones, the
-// merge included, 319 to 327 us by graph replay or 800 TFLOP/s, half of what a library product of
+// merge included, 318 to 327 us by graph replay or 800 TFLOP/s, half of what a library product of
 // 8192^3 reaches here (floor 156 us).  At 1 x 1024 the kernel takes 187 us under the profiler with 38 %
 // of the tensor and of the exp2 pipe busy, the warps waiting for TMEM loads: a stream's tile is a
 // chain of products, their commit, four rounds of load, exp2 and store, and the next products.  TMEM
